@@ -249,8 +249,8 @@ def _quantise(x):
     group's largest magnitude."""
     g = x.unflatten(-1, (-1, 16))
     top = g.abs().amax(-1)
-    every = _scale_values(torch.arange(0, 226, dtype=torch.uint8, device=x.device))  # 225 is the largest one used
-    byte = torch.searchsorted(7.0 * every, top.contiguous()).clamp(max=225)
+    every = _scale_values(torch.arange(0, 211, dtype=torch.uint8, device=x.device))  # 210, which is 2560, is the largest one used
+    byte = torch.searchsorted(7.0 * every, top.contiguous()).clamp(max=210)
     scale = every[byte][..., None]
     u = torch.where(scale > 0, g / scale, torch.zeros_like(g)).round().clamp(-7, 7).to(torch.int32) + 8
     u = u.flatten(-2).unflatten(-1, (-1, 4, 2))  # [..][word][j][dim 2 j or 2 j + 1]
@@ -413,7 +413,7 @@ def _held64(x):
     need = g.abs().amax(-1, keepdim=True) / 7
     _, e = torch.frexp(need)  # need = m 2^e, 0.5 <= m < 1
     grain = torch.exp2((e - 1).clamp(min=-14).double() - 3)  # the spacing of scales there
-    size = (torch.ceil(need / grain) * grain).clamp(max=9216.0)
+    size = (torch.ceil(need / grain) * grain).clamp(max=2560.0)
     return torch.where(size > 0, torch.round(g / size).clamp(-7, 7) * size, torch.zeros_like(g)).reshape(x.shape)
 
 
