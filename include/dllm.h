@@ -293,6 +293,122 @@ int dllm_op_lm_head_conf(const uint16_t* y, const uint16_t* head, int T, int d, 
 int dllm_op_lm_head_conf_noalloc(const uint16_t* y, const uint16_t* head, int T, int d, int V, int mask_id,
                                  float* conf, int32_t* argmax, void* stream);
 
+/* ---- rotary positions and the paged 4-bit KV cache --------------------------------
+ * Single operations for a KV cache held in 4 bits and in pages: rotate queries
+ * (dllm_op_rope), append keys and values with the rotation on the way
+ * (dllm_op_append_kv4), attend to the cache (dllm_op_attn_kv4) and read it back
+ * (dllm_op_read_kv4). The pages have no counterpart; the operations serve callers that keep
+ * more or longer requests than bf16 slots hold (0.5625 bytes per value instead of 2).
+ * As above: device pointers, work queued on `stream` of the current device, no allocation,
+ * no synchronisation, capturable in a CUDA graph. Nothing is kept between calls. Sizes are
+ * checked on the host (DLLM_E_INVAL, nothing queued); what lies in device memory is checked
+ * by the kernels, as each call says. Strides are in elements; the last dimension is
+ * contiguous. */
+#define DLLM_F32 0
+#define DLLM_BF16 1
+
+#define DLLM_ROPE_HALF 0         /* pairs (i, i + rotary_dim / 2) */
+#define DLLM_ROPE_INTERLEAVED 1  /* pairs (2 i, 2 i + 1) */
+#define DLLM_ROPE_NONE 0
+#define DLLM_ROPE_LINEAR 1
+#define DLLM_ROPE_NTK 2
+#define DLLM_ROPE_YARN 3
+#define DLLM_ROPE_MAX_PAIRS 128
+
+/* A rotation plan: pair i of the first rotary_dim dims of a head turns by turns[i] * position,
+ * and the rotated dims are scaled by magnitude. An ordinary host struct, filled by
+ * dllm_rope_init and copied into each launch; no device memory. */
+typedef struct {
+  int rotary_dim;
+  int layout;
+  double magnitude;
+  double turns[DLLM_ROPE_MAX_PAIRS];
+} dllm_rope;
+
+/* Fills a plan. rotary_dim: even, 2 .. 256. Angle of pair i per position:
+ *   NONE    theta^(-2 i / rotary_dim);
+ *   LINEAR  that / factor (positions interpolated);
+ *   NTK     theta * factor^(rotary_dim / (rotary_dim - 2)) in place of theta (rotary_dim >= 4);
+ *   YARN    by parts: pairs that turn more than beta_fast times over original_ctx positions keep
+ *           NONE's angle, pairs below beta_slow turns take LINEAR's, a linear ramp over the pair
+ *           index lies between; magnitude = 0.1 ln(factor) + 1 (else 1).
+ * factor >= 1 (NONE ignores it); original_ctx, beta_fast and beta_slow are YARN's alone. */
+int dllm_rope_init(dllm_rope* out, int rotary_dim, int layout, double theta, int scaling, double factor,
+                   double original_ctx, double beta_fast, double beta_slow);
+
+/* y[t][h] = x[t][h] rotated to position pos[t] (device int32 [T]); dims from rotary_dim on are
+ * copied. x and y are DLLM_F32 or DLLM_BF16, each with its own strides, head_dim <= 1024.
+ * y == x with equal type and strides is allowed; other overlaps are not. transposed = 1
+ * applies the transposed map, which is the gradient: with dy given as x it writes dx to y.
+ * Angles are reduced in 64 bits, cos and sin rounded to fp32 once, products and sums in fp32,
+ * one rounding to y's type. T = 0 queues nothing. */
+int dllm_op_rope(const dllm_rope* rope, const void* x, int x_type, long long x_token_stride,
+                 long long x_head_stride, const int32_t* pos, int T, int H, int head_dim, void* y, int y_type,
+                 long long y_token_stride, long long y_head_stride, int transposed, void* stream);
+
+/* A paged 4-bit cache of one layer (a host struct; the arrays are the caller's, 16-byte aligned):
+ *   codes  uint8 [n_pages][2][n_kv_heads][page][head_dim / 2]    ([2]: K, V)
+ *   scales uint8 [n_pages][2][n_kv_heads][page][head_dim / 16]
+ * page: 16, 32, 64, 128 or 256 positions; head_dim: 64, 128 or 176; n_pages * page < 2^31.
+ * A scale byte b is shared by 16 consecutive dims and means the fp16 number with bits b << 7;
+ * a dim's value is scale * (code - 8). The codes of dims 8 w .. 8 w + 7 are one little-endian
+ * 32-bit word: dim 8 w + 2 j is nibble j, dim 8 w + 2 j + 1 nibble j + 4. Appending writes the
+ * least scale with 7 * scale >= the group's largest magnitude and the nearest code in 1 .. 15
+ * (ties to even); magnitudes beyond 17920 saturate, NaN is stored as 0. Every value is exact
+ * in bf16.
+ * Page tables are device int32 [rows][table_stride]: position p of row r lies in page
+ * table[r][p / page]. Rows may share pages (a common prefix), and layers may share a table. */
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  int n_pages, page, n_kv_heads, head_dim;
+} dllm_kv4;
+
+/* Writes token t's keys k[t][n_kv_heads][head_dim], rotated by `rope` (NULL: as they are) to
+ * position rope_pos[t] (NULL: pos[t]), and values v[t][...] to position pos[t] of table row
+ * req[t] (all device int32 [T]). k and v are of one type with their own strides, e.g. slices of
+ * a fused QKV result. Positions written before are overwritten (a canvas written anew every
+ * pass). A token with req < 0 is padding and skipped, whatever its other inputs hold; so is one
+ * whose row, position or page does not exist. The positions that one call writes must differ:
+ * of two tokens at one position each byte is one of theirs. */
+int dllm_op_append_kv4(const dllm_kv4* cache, const void* k, long long k_token_stride, long long k_head_stride,
+                       const void* v, long long v_token_stride, long long v_head_stride, int type,
+                       const int32_t* req, const int32_t* pos, const int32_t* rope_pos, int T, const int32_t* table,
+                       int n_req, int table_stride, const dllm_rope* rope, void* stream);
+
+/* Reads positions back as bf16: k_out and v_out [T][n_kv_heads][head_dim], contiguous and 16-byte
+ * aligned, either may be NULL. Token t is position pos[t] of row req[t]; req < 0: its rows of the
+ * outputs are left as they were; a row, position or page that does not exist reads NaN. */
+int dllm_op_read_kv4(const dllm_kv4* cache, const int32_t* req, const int32_t* pos, int T, const int32_t* table,
+                     int n_req, int table_stride, uint16_t* k_out, uint16_t* v_out, void* stream);
+
+/* Attention of a batch's queries over the cache. Request b's queries are rows q_start[b] ..
+ * q_start[b + 1] - 1 of q (bf16 [T][H][head_dim] with strides that are multiples of 8, 16-byte
+ * aligned) and it sees positions 0 .. kv_len[b] - 1 of table row b: all of them, or with
+ * causal = 1 query i of n those below kv_len[b] - n + i + 1 (its queries are the last n
+ * positions). q_start [B + 1] and kv_len [B] are device int32. H is a multiple of n_kv_heads;
+ * query head h reads KV head h / (H / n_kv_heads).
+ *   out[t][h] (bf16, strides as q's) = softmax(scale * q k^T) v; a row that sees no key is 0.
+ *   lse[t][h] (fp32 [T][H], or NULL) = the natural log of the sum of exp(scale * q k), -inf for a
+ *   row that sees no key: it joins this result with attention over other keys.
+ * Rows of q that no request covers are left as they were in out and lse. max_q and max_kv are the
+ * caller's bounds on the requests' queries and keys (max_q <= T, max_kv < 2^29). A request that
+ * exceeds them or its row of the table, or with kv_len < 0, gets NaN in all its rows; one whose
+ * q_start range is not within 0 .. T is skipped; a page id outside the cache gives NaN in the
+ * rows that see it (other rows of that request may be NaN too), as does a kernel that gives
+ * up a bounded wait.
+ * workspace: dllm_op_attn_kv4_workspace's bytes for the same sizes (0 at times), 16-byte
+ * aligned; it holds partial results only while the call runs, so calls that may overlap on the
+ * GPU, graphs that hold them included, need one each. */
+int dllm_op_attn_kv4(const dllm_kv4* cache, const uint16_t* q, long long q_token_stride, long long q_head_stride,
+                     uint16_t* out, long long out_token_stride, long long out_head_stride, float* lse,
+                     const int32_t* q_start, const int32_t* kv_len, int B, int T, int max_q, int max_kv, int H,
+                     const int32_t* table, int table_stride, int causal, float scale, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of dllm_op_attn_kv4 with these sizes, or DLLM_E_INVAL. */
+long long dllm_op_attn_kv4_workspace(const dllm_kv4* cache, int B, int T, int max_q, int max_kv, int H);
+
 #ifdef __cplusplus
 }
 #endif

@@ -3,7 +3,9 @@
 The denoising pass, prefill, append and the commit sampler run in libdllm.so
 (hand-written sm_100a CUDA kernels behind the C ABI of include/dllm.h). This package
 holds the ctypes binding (``binding``) and ``Denoiser``, a thin torch-facing wrapper
-that only moves pointers, sizes and streams across the ABI.
+that only moves pointers, sizes and streams across the ABI. ``Rope``, ``rope`` and
+``KVCache4`` (module ``kv4``) are the same for the single operations on rotary positions and
+the paged 4-bit KV cache.
 """
 
 from __future__ import annotations
@@ -15,7 +17,16 @@ import numpy as np
 from . import binding
 from .binding import (DllmError, dllm_config, dllm_policy, make_config, make_policy)
 
-__all__ = ["binding", "Denoiser", "DllmError", "dllm_config", "dllm_policy", "make_config", "make_policy"]
+__all__ = ["binding", "Denoiser", "DllmError", "KVCache4", "Rope", "dllm_config", "dllm_policy", "make_config",
+           "make_policy", "rope"]
+
+
+def __getattr__(name):
+    # kv4 works on torch tensors; the package itself imports torch only when it is used
+    if name in ("KVCache4", "Rope", "rope"):
+        from . import kv4
+        return getattr(kv4, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 class Denoiser:

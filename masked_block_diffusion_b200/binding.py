@@ -39,7 +39,18 @@ EXPORTS = [
     "dllm_set_debug", "dllm_debug_read", "dllm_debug_force_routing", "dllm_last_error", "dllm_destroy",
     "dllm_op_gemm_bf16", "dllm_op_lm_head_conf", "dllm_op_lm_head_conf_noalloc", "dllm_set_timing",
     "dllm_timing_read", "dllm_set_wait_limit", "dllm_append_kv_approx", "dllm_op_quantize_fp8",
+    "dllm_rope_init", "dllm_op_rope", "dllm_op_append_kv4", "dllm_op_read_kv4", "dllm_op_attn_kv4",
+    "dllm_op_attn_kv4_workspace",
 ]
+DLLM_F32 = 0
+DLLM_BF16 = 1
+DLLM_ROPE_HALF = 0
+DLLM_ROPE_INTERLEAVED = 1
+DLLM_ROPE_NONE = 0
+DLLM_ROPE_LINEAR = 1
+DLLM_ROPE_NTK = 2
+DLLM_ROPE_YARN = 3
+DLLM_ROPE_MAX_PAIRS = 128
 DLLM_TIMING_GATE_UP = 0
 DLLM_TIMING_DOWN = 1
 DLLM_TIMING_ATTN = 2
@@ -70,6 +81,16 @@ class dllm_policy(ctypes.Structure):
                 ("t2t", ctypes.c_int), ("edit_tau", ctypes.c_float)]
 
 
+class dllm_rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int), ("magnitude", ctypes.c_double),
+                ("turns", ctypes.c_double * DLLM_ROPE_MAX_PAIRS)]
+
+
+class dllm_kv4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("page", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
 class DllmError(RuntimeError):
     def __init__(self, code: int, where: str, msg: str = ""):
         super().__init__(f"{where} failed: {ERROR_NAMES.get(code, code)} {msg}".strip())
@@ -80,6 +101,8 @@ _lib: Optional[ctypes.CDLL] = None
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
+_d = ctypes.c_double
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -114,6 +137,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "dllm_set_wait_limit": (_i, [_vp, ctypes.c_longlong]),
         "dllm_append_kv_approx": (_i, [_vp, _i]),
         "dllm_op_quantize_fp8": (_i, [_vp, _i, _i, _vp, _vp, _vp]),
+        "dllm_rope_init": (_i, [ctypes.POINTER(dllm_rope), _i, _i, _d, _i, _d, _d, _d, _d]),
+        "dllm_op_rope": (_i, [ctypes.POINTER(dllm_rope), _vp, _i, _ll, _ll, _vp, _i, _i, _i, _vp, _i, _ll, _ll, _i,
+                              _vp]),
+        "dllm_op_append_kv4": (_i, [ctypes.POINTER(dllm_kv4), _vp, _ll, _ll, _vp, _ll, _ll, _i, _vp, _vp, _vp, _i, _vp,
+                                    _i, _i, ctypes.POINTER(dllm_rope), _vp]),
+        "dllm_op_read_kv4": (_i, [ctypes.POINTER(dllm_kv4), _vp, _vp, _i, _vp, _i, _i, _vp, _vp, _vp]),
+        "dllm_op_attn_kv4": (_i, [ctypes.POINTER(dllm_kv4), _vp, _ll, _ll, _vp, _ll, _ll, _vp, _vp, _vp, _i, _i, _i, _i,
+                                  _i, _vp, _i, _i, ctypes.c_float, _vp, ctypes.c_size_t, _vp]),
+        "dllm_op_attn_kv4_workspace": (_ll, [ctypes.POINTER(dllm_kv4), _i, _i, _i, _i, _i]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -268,3 +300,46 @@ def dllm_op_quantize_fp8(w_ptr, rows, cols, q_ptr, exps_ptr, stream_ptr):
     """FP8 E4M3 codes and per-128x128-tile scale exponents of a bf16 matrix (device buffers)."""
     _check(load().dllm_op_quantize_fp8(_vp(w_ptr), rows, cols, _vp(q_ptr), _vp(exps_ptr), _vp(stream_ptr)),
            "dllm_op_quantize_fp8")
+
+
+def dllm_rope_init(rotary_dim, layout, theta, scaling, factor, original_ctx, beta_fast, beta_slow) -> dllm_rope:
+    r = dllm_rope()
+    _check(load().dllm_rope_init(ctypes.byref(r), rotary_dim, layout, theta, scaling, factor, original_ctx, beta_fast,
+                                 beta_slow), "dllm_rope_init")
+    return r
+
+
+def dllm_op_rope(rope: dllm_rope, x_ptr, x_type, x_token_stride, x_head_stride, pos_ptr, T, H, head_dim, y_ptr, y_type,
+                 y_token_stride, y_head_stride, transposed, stream_ptr):
+    _check(load().dllm_op_rope(rope, x_ptr, x_type, x_token_stride, x_head_stride, pos_ptr, T, H, head_dim, y_ptr,
+                               y_type, y_token_stride, y_head_stride, transposed, stream_ptr), "dllm_op_rope")
+
+
+def dllm_op_append_kv4(cache: dllm_kv4, k_ptr, k_token_stride, k_head_stride, v_ptr, v_token_stride, v_head_stride, type_,
+                       req_ptr, pos_ptr, rope_pos_ptr, T, table_ptr, n_req, table_stride, rope, stream_ptr):
+    """rope: a dllm_rope or None; rope_pos_ptr 0: pos."""
+    _check(load().dllm_op_append_kv4(cache, k_ptr, k_token_stride, k_head_stride, v_ptr, v_token_stride, v_head_stride,
+                                     type_, req_ptr, pos_ptr, rope_pos_ptr, T, table_ptr, n_req, table_stride, rope,
+                                     stream_ptr), "dllm_op_append_kv4")
+
+
+def dllm_op_read_kv4(cache: dllm_kv4, req_ptr, pos_ptr, T, table_ptr, n_req, table_stride, k_out_ptr, v_out_ptr,
+                     stream_ptr):
+    _check(load().dllm_op_read_kv4(cache, req_ptr, pos_ptr, T, table_ptr, n_req, table_stride, k_out_ptr, v_out_ptr,
+                                   stream_ptr), "dllm_op_read_kv4")
+
+
+def dllm_op_attn_kv4(cache: dllm_kv4, q_ptr, q_token_stride, q_head_stride, out_ptr, out_token_stride, out_head_stride,
+                     lse_ptr, q_start_ptr, kv_len_ptr, B, T, max_q, max_kv, H, table_ptr, table_stride, causal, scale,
+                     workspace_ptr, workspace_bytes, stream_ptr):
+    _check(load().dllm_op_attn_kv4(cache, q_ptr, q_token_stride, q_head_stride, out_ptr, out_token_stride,
+                                   out_head_stride, lse_ptr, q_start_ptr, kv_len_ptr, B, T, max_q, max_kv, H, table_ptr,
+                                   table_stride, causal, scale, workspace_ptr, workspace_bytes, stream_ptr),
+           "dllm_op_attn_kv4")
+
+
+def dllm_op_attn_kv4_workspace(cache: dllm_kv4, B, T, max_q, max_kv, H) -> int:
+    n = load().dllm_op_attn_kv4_workspace(cache, B, T, max_q, max_kv, H)
+    if n < 0:
+        _check(n, "dllm_op_attn_kv4_workspace")
+    return n

@@ -16,7 +16,13 @@ SYNTH_SRC = os.path.join(ROOT, "synth", "csrc", "synth_fill.cu")
 SYNTH_LIB = os.path.join(ROOT, "synth", "libsynth.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-COMMON = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC", "-shared"]
+COMMON = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC"]
+# the library's translation units, compiled side by side, and the headers each one reads
+UNITS = {
+    "engine": ["attention.cuh", "attention_tc.cuh", "common.cuh", "gemm_tc.cuh", "kernels.cuh"],
+    "kv4": ["attention.cuh", "attention_tc.cuh", "common.cuh", "attention_kv4.cuh", "kv4.cuh", "rope.cuh"],
+}
+OBJ = os.path.join(PKG, "_build")
 
 
 def nvcc() -> str:
@@ -34,19 +40,35 @@ def _stale(target: str, sources) -> bool:
 
 
 def build_dllm(force: bool = False, verbose_ptxas: bool = False) -> str:
-    srcs = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC))] + [os.path.join(INCLUDE, "dllm.h")]
-    if force or _stale(LIB, srcs):
-        cmd = [nvcc(), *ARCH, *COMMON, "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, "engine.cu"), "-o", LIB + ".tmp"]
+    os.makedirs(OBJ, exist_ok=True)
+    objs, running = [], []
+    for name, headers in UNITS.items():
+        obj = os.path.join(OBJ, name + ".o")
+        objs.append(obj)
+        srcs = [os.path.join(CSRC, f) for f in [name + ".cu", *headers]] + [os.path.join(INCLUDE, "dllm.h")]
+        # without its object files (a tree that got the library alone) the library's own age counts
+        if not force and not _stale(obj if os.path.exists(obj) else LIB, srcs):
+            continue
+        cmd = [nvcc(), *ARCH, *COMMON, "-c", "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, name + ".cu"), "-o", obj + ".tmp"]
         if verbose_ptxas:
             cmd.insert(1, "-Xptxas=-v")
-        subprocess.run(cmd, check=True)
+        running.append((subprocess.Popen(cmd), cmd, obj))
+    for p, cmd, obj in running:
+        if p.wait() != 0:
+            raise subprocess.CalledProcessError(p.returncode, cmd)
+        os.replace(obj + ".tmp", obj)
+    if running or not os.path.exists(LIB):
+        missing = [o for o in objs if not os.path.exists(o)]
+        if missing:
+            return build_dllm(True, verbose_ptxas)
+        subprocess.run([nvcc(), *ARCH, "-shared", *objs, "-o", LIB + ".tmp"], check=True)
         os.replace(LIB + ".tmp", LIB)
     return LIB
 
 
 def build_synth(force: bool = False) -> str:
     if force or _stale(SYNTH_LIB, [SYNTH_SRC]):
-        cmd = [nvcc(), *ARCH, *COMMON, SYNTH_SRC, "-o", SYNTH_LIB + ".tmp"]
+        cmd = [nvcc(), *ARCH, *COMMON, "-shared", SYNTH_SRC, "-o", SYNTH_LIB + ".tmp"]
         subprocess.run(cmd, check=True)
         os.replace(SYNTH_LIB + ".tmp", SYNTH_LIB)
     return SYNTH_LIB

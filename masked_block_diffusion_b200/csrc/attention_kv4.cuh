@@ -1,0 +1,498 @@
+// Attention over the paged 4-bit KV cache for few query rows per KV head (single tokens, a
+// few tokens to verify, small canvases), and the merge of key splits.
+//
+// Row R of request b and KV head g is query R / group, head g * group + R % group. Row R
+// sees the keys below lim = kv_len (causal: kv_len - n + R / group + 1 for n queries):
+//   s_t = scale * q . k_t,   o = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m),   lse = m + log(sum).
+// A row that sees no key has o = 0 and lse = -inf.
+//
+// With few rows the packed cache's bytes bound the time, if unpacking them does not: both
+// products are taken transposed, S^T = K Q^T and O^T = V^T P^T, so that the packed operand
+// fills the 16-row side of mma.m16n8k16 and eight query rows its 8-column side. (The 5th-
+// generation tensor instruction reads its operands from shared or tensor memory only; with
+// rows this few, writing the unpacked values there and reading them back would cost more
+// than the multiplication.) Unpacking is an AND, an OR and one exact fma per two values plus
+// a shift. Thread (r, c) = (lane / 4, lane % 4):
+//   K: token r's and token r + 8's dims 64 i + 16 c .. + 15 (8 code bytes and their scale) are
+//      its A fragments of four k16 steps; Q's fragments carry the same dims.
+//   V: tokens 2c, 2c + 1, 2c + 8, 2c + 9, dims 8 w .. 8 w + 7 with w = 8 i + r: a byte permute
+//      pairs two tokens' words, and nibble pair j gives the two tokens' dim 8 w + 2 j (+ 1).
+// P is rounded to fp16 (11 bits) for O^T; the running maximum is kept 6 octaves low, so that
+// P up to 2^14 uses fp16's range and weights down to 2^-30 of the largest survive. Scores,
+// sums and accumulators are fp32.
+#pragma once
+
+#include "common.cuh"
+#include "attention_tc.cuh"
+#include "kv4.cuh"
+
+namespace dllm {
+
+constexpr float kKv4Low = 6.f;    // the softmax reference lies this many octaves below the maximum seen
+
+struct AttnKv4Params {
+  Kv4 c;
+  const bf16_t* q;
+  long q_tok, q_head;
+  bf16_t* out;
+  long o_tok, o_head;
+  float* lse;               // [T][H] or null
+  const int* q_start;       // [B + 1]
+  const int* kv_len;        // [B]
+  const int* table;         // [B][stride]
+  int stride, B, T, H, group;
+  int max_q, max_kv, causal;
+  int n_splits, chunk;      // keys [i chunk, (i + 1) chunk) belong to split i; chunk % 64 == 0
+  float scale_log2;         // scale * log2(e)
+  float* part_o;            // [n_splits][T][H][hd]
+  float* part_lse;          // [n_splits][T][H], log2 domain
+};
+
+// A request's queries and keys. bad: its row range holds, but not its lengths: every row becomes NaN.
+struct Kv4Req {
+  int q0, n, kv;
+  bool skip, bad;
+};
+
+DLLM_DEV Kv4Req kv4_request(const AttnKv4Params& p, int b) {
+  Kv4Req r;
+  r.q0 = p.q_start[b];
+  const int q1 = p.q_start[b + 1];
+  r.kv = p.kv_len[b];
+  r.skip = r.q0 < 0 || q1 < r.q0 || q1 > p.T;
+  r.n = r.skip ? 0 : q1 - r.q0;
+  const long room = (long)p.stride << p.c.page_shift;
+  r.bad = r.n > p.max_q || r.kv < 0 || r.kv > p.max_kv || r.kv > room;
+  return r;
+}
+
+// Row R's keys end here.
+DLLM_DEV int kv4_row_limit(const AttnKv4Params& p, const Kv4Req& r, int query) {
+  return p.causal ? max(0, min(r.kv, r.kv - r.n + query + 1)) : r.kv;
+}
+
+// Every row of a bad request's head range [h0, h0 + nh) becomes NaN.
+DLLM_DEV void kv4_poison(const AttnKv4Params& p, const Kv4Req& r, int h0, int nh, int hd) {
+  const long total = (long)r.n * nh * hd;
+  for (long u = threadIdx.x; u < total; u += blockDim.x) {
+    const long row = u / hd;
+    const long t = r.q0 + row / nh;
+    const int h = h0 + (int)(row % nh), d = (int)(u - row * hd);
+    p.out[t * p.o_tok + h * p.o_head + d] = 0x7FC0;
+    if (d == 0 && p.lse != nullptr) p.lse[t * p.H + h] = __int_as_float(0x7FC00000);
+  }
+}
+
+DLLM_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"((uint64_t)__cvta_generic_to_global(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+DLLM_DEV void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 matrix of 16-bit values held two per thread.
+DLLM_DEV uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// Two fp16 values of nibble pair j: 16 + u in fp16 (u at mantissa bits 6..9), then (16 + u) s - 24 s, exact.
+DLLM_DEV uint32_t kv4_f16x2(uint32_t w, int j, __half2 s, __half2 ms24) {
+  const uint32_t sh = j == 0 ? w << 6 : j == 1 ? w << 2 : w >> (4 * j - 6);
+  const uint32_t u = (sh & 0x03C003C0u) | 0x4C004C00u;
+  const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&u), s, ms24);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+DLLM_DEV __half2 kv4_half2(uint32_t bits) { return *reinterpret_cast<const __half2*>(&bits); }
+
+// Shared memory of a block: `STAGES` stages of 64 keys' packed K and V; four consumer warps
+// take 16 keys each, a fifth warp issues the copies. 48 KB or less, so that several blocks
+// share an SM and keep enough bytes in flight.
+template <int HD, int NR>
+struct AttnKv4Cfg {
+  static constexpr int KEYS = 64;
+  static constexpr int WARPS = 4;
+  static constexpr int kCodes = KEYS * HD / 2;
+  static constexpr int kScales = KEYS * HD / 16;
+  static constexpr int kStage = 2 * (kCodes + kScales);
+  static constexpr int STAGES = HD == 64 ? 8 : 4;
+  static constexpr int kRows = 8 * NR;
+  static constexpr int kRed = WARPS * kRows * (HD + 2) * 4;     // the warps' results, over the stages
+  static constexpr int kBody = STAGES * kStage > kRed ? STAGES * kStage : kRed;
+  static constexpr int kOffBar = (kBody + 15) / 16 * 16;
+  static constexpr int kTotal = kOffBar + 2 * STAGES * 8 + 16;
+  static constexpr int THREADS = 32 * (WARPS + 1);
+};
+
+// Grid (n_splits, Hkv * row tiles, B). A block takes 8 NR rows of one KV head over one split.
+template <int HD, int NR>
+__global__ void __launch_bounds__(AttnKv4Cfg<HD, NR>::THREADS, NR == 1 ? 3 : 2)
+attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
+  using G = AttnKv4Cfg<HD, NR>;
+  constexpr int KI = (HD + 63) / 64;
+  constexpr int WORDS = HD / 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);
+  uint64_t* empty = full + G::STAGES;
+  volatile int* flags = reinterpret_cast<volatile int*>(empty + G::STAGES);   // [0] abort, [1] a page that is none
+
+  pdl_begin();
+  const int g = blockIdx.y % p.c.Hkv, tile = blockIdx.y / p.c.Hkv, sp = blockIdx.x, b = blockIdx.z;
+  const Kv4Req rq = kv4_request(p, b);
+  const int R0 = tile * G::kRows, n_rows = rq.n * p.group;
+  if (rq.skip) return;
+  if (rq.bad) {
+    if (tile == 0 && sp == 0) kv4_poison(p, rq, g * p.group, p.group, HD);
+    return;
+  }
+  if (R0 >= n_rows) return;
+  const int last = min(n_rows - 1, R0 + G::kRows - 1);
+  const int ks = sp * p.chunk;
+  const int ke = min(kv4_row_limit(p, rq, last / p.group), ks + p.chunk);
+  const int nst = ke > ks ? (ke - ks + G::KEYS - 1) / G::KEYS : 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < G::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], G::WARPS);
+    }
+    flags[0] = flags[1] = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  if (warp == G::WARPS) {
+    // ---------------- producer: lane i copies piece i of a stage (a page's share of it)
+    const int shift = min(p.c.page_shift, 6);
+    const int pieces = G::KEYS >> shift, keys = 1 << shift;
+    const uint32_t codes = keys * HD / 2, scales = keys * HD / 16;
+    const int* row = p.table + (long)b * p.stride;
+    bool ok = true;
+    int it = 0;
+    for (; it < nst; ++it) {
+      const int t = ks + it * G::KEYS + lane * keys;
+      int id = -1;
+      const bool want = lane < pieces && t < ke;
+      if (want) {
+        id = row[t >> p.c.page_shift];
+        if (id < 0 || id >= p.c.n_pages) {
+          id = -1;
+          flags[1] = 1;
+        }
+      }
+      const uint32_t n = __popc(__ballot_sync(0xffffffffu, id >= 0));
+      const int st = it % G::STAGES;
+      if (!mbar_wait(&empty[st], ((it / G::STAGES) & 1) ^ 1, flags)) ok = false;
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], n * 2 * (codes + scales));
+      __syncwarp();
+      if (id >= 0) {
+        uint8_t* dst = smem + st * G::kStage;
+        const int off = t & ((1 << p.c.page_shift) - 1);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const long r = kv4_row(p.c, id, kv, g, off);
+          uint8_t* d = dst + kv * (G::kCodes + G::kScales);
+          bulk_load(d + lane * codes, p.c.codes + r * (HD / 2), codes, &full[st]);
+          bulk_load(d + G::kCodes + lane * scales, p.c.scales + r * (HD / 16), scales, &full[st]);
+        }
+      }
+    }
+    if (!__all_sync(0xffffffffu, ok)) flags[0] = 1;
+    // whatever the consumers did, the copies already issued land before the stages are used otherwise
+    for (int j = max(0, it - G::STAGES); j < it; ++j) mbar_drain(&full[j % G::STAGES], (j / G::STAGES) & 1);
+    __syncthreads();
+  } else {
+    // ---------------- consumers
+    const int r = lane >> 2, c = lane & 3;
+    uint32_t qf[NR][KI][8];
+    int lim[NR][2];                       // columns 2c, 2c + 1: keys the row sees end here
+    float m[NR][2], l[NR][2];
+    float o[NR][KI][4][4];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      const int R = R0 + 8 * nr + r;
+      const bool real = R < n_rows;
+      const bf16_t* qr = p.q + (long)(rq.q0 + (real ? R / p.group : 0)) * p.q_tok + (g * p.group + (real ? R % p.group : 0)) * p.q_head;
+#pragma unroll
+      for (int i = 0; i < KI; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int d = 64 * i + 16 * c + 8 * h;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (real && d < HD) v = *reinterpret_cast<const uint4*>(qr + d);
+          qf[nr][i][4 * h] = v.x;
+          qf[nr][i][4 * h + 1] = v.y;
+          qf[nr][i][4 * h + 2] = v.z;
+          qf[nr][i][4 * h + 3] = v.w;
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int Rc = R0 + 8 * nr + 2 * c + e;
+        lim[nr][e] = Rc < n_rows ? min(ke, kv4_row_limit(p, rq, Rc / p.group)) : 0;
+        m[nr][e] = -INFINITY;
+        l[nr][e] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < KI; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nr][i][j][e] = 0.f;
+    }
+
+    bool ok = true;
+    for (int it = 0; it < nst; ++it) {
+      const int st = it % G::STAGES;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (it / G::STAGES) & 1, flags))) { ok = false; break; }
+      const int t0 = ks + it * G::KEYS + 16 * warp;
+      if (t0 < ke) {
+        const uint8_t* kc = smem + st * G::kStage + 16 * warp * (HD / 2);
+        const uint8_t* kS = smem + st * G::kStage + G::kCodes + 16 * warp * (HD / 16);
+        const uint8_t* vc = kc + G::kCodes + G::kScales;
+        const uint8_t* vS = kS + G::kCodes + G::kScales;
+        float s[NR][4];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nr][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+          const int grp = 4 * i + c;
+          const bool in = 16 * grp < HD;
+          uint2 wa = make_uint2(0, 0), wb = wa;
+          uint32_t ba = 0, bb = 0;
+          if (in) {
+            wa = *reinterpret_cast<const uint2*>(kc + r * (HD / 2) + 8 * grp);
+            wb = *reinterpret_cast<const uint2*>(kc + (r + 8) * (HD / 2) + 8 * grp);
+            ba = kS[r * (HD / 16) + grp];
+            bb = kS[(r + 8) * (HD / 16) + grp];
+          }
+          const __nv_bfloat162 m24 = __float2bfloat162_rn(-24.f);
+          const __nv_bfloat162 sa = kv4_scale_bf16x2(ba), sb = kv4_scale_bf16x2(bb);
+          const __nv_bfloat162 na = __hmul2(sa, m24), nb = __hmul2(sb, m24);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t xa = h ? wa.y : wa.x, xb = h ? wb.y : wb.x;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t a[4] = {kv4_bf16x2(xa, 2 * k, sa, na), kv4_bf16x2(xb, 2 * k, sb, nb),
+                                     kv4_bf16x2(xa, 2 * k + 1, sa, na), kv4_bf16x2(xb, 2 * k + 1, sb, nb)};
+#pragma unroll
+              for (int nr = 0; nr < NR; ++nr)
+                mma_bf16_16816(s[nr], a, qf[nr][i][4 * h + 2 * k], qf[nr][i][4 * h + 2 * k + 1]);
+            }
+          }
+        }
+        uint32_t pf[NR][2];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[nr][e] *= p.scale_log2;
+            if (t0 + r + 8 * (e >> 1) >= lim[nr][e & 1]) s[nr][e] = -INFINITY;
+          }
+          const float mx0 = fmaxf(s[nr][0], s[nr][2]), mx1 = fmaxf(s[nr][1], s[nr][3]);
+          // a new reference only when a score is more than 2^14 above it (the first visible key always is)
+          if (__any_sync(0xffffffffu, mx0 > m[nr][0] + (kKv4Low + 8.f) || mx1 > m[nr][1] + (kKv4Low + 8.f))) {
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = e ? mx1 : mx0;
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              const float mn = fmaxf(m[nr][e], mx - kKv4Low);
+              f[e] = mn == -INFINITY ? 1.f : exp2f(m[nr][e] - mn);
+              m[nr][e] = mn;
+              l[nr][e] *= f[e];
+            }
+#pragma unroll
+            for (int i = 0; i < KI; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nr][i][j][e] *= f[e & 1];
+          }
+          const float b0 = m[nr][0] == -INFINITY ? 0.f : m[nr][0], b1 = m[nr][1] == -INFINITY ? 0.f : m[nr][1];
+          const float p0 = ex2_approx(s[nr][0] - b0), p1 = ex2_approx(s[nr][1] - b1);
+          const float p2 = ex2_approx(s[nr][2] - b0), p3 = ex2_approx(s[nr][3] - b1);
+          l[nr][0] += p0 + p2;
+          l[nr][1] += p1 + p3;
+          const __half2 h01 = __floats2half2_rn(p0, p1), h23 = __floats2half2_rn(p2, p3);
+          pf[nr][0] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h01));
+          pf[nr][1] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h23));
+        }
+        const bool tail = t0 + 16 > ke;   // keys past the end: what their bytes hold is not used, not even times 0
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+          const int w = 8 * i + r;
+          const bool in = w < WORDS;
+          uint32_t x[4], sc[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = 2 * c + (e & 1) + 8 * (e >> 1);
+            x[e] = 0;
+            sc[e] = 0;
+            if (in) {
+              x[e] = *reinterpret_cast<const uint32_t*>(vc + t * (HD / 2) + 4 * w);
+              sc[e] = vS[t * (HD / 16) + w / 2];
+            }
+            if (tail && t0 + t >= ke) sc[e] = 0;
+          }
+          const __half2 m24 = __float2half2_rn(-24.f);
+          const __half2 s0 = kv4_half2((sc[0] << 7) | (sc[1] << 23)), s1 = kv4_half2((sc[2] << 7) | (sc[3] << 23));
+          const __half2 n0 = __hmul2(s0, m24), n1 = __hmul2(s1, m24);
+          const uint32_t e0 = __byte_perm(x[0], x[1], 0x5410), d0 = __byte_perm(x[0], x[1], 0x7632);
+          const uint32_t e1 = __byte_perm(x[2], x[3], 0x5410), d1 = __byte_perm(x[2], x[3], 0x7632);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a[4] = {kv4_f16x2(e0, j, s0, n0), kv4_f16x2(d0, j, s0, n0), kv4_f16x2(e1, j, s1, n1),
+                                   kv4_f16x2(d1, j, s1, n1)};
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) mma_f16_16816(o[nr][i][j], a, pf[nr][0], pf[nr][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+    if (!ok) flags[0] = 1;
+    __syncthreads();   // every copy has landed and every stage is read: the stages' memory is free
+    // ---------------- each warp's reference, sum and O of its rows
+    float* red = reinterpret_cast<float*>(smem) + warp * G::kRows * (HD + 2);
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[nr][e];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        float* row = red + (8 * nr + 2 * c + e) * (HD + 2);
+        if (r == 0) {
+          row[HD] = m[nr][e];
+          row[HD + 1] = sum;
+        }
+#pragma unroll
+        for (int i = 0; i < KI; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (8 * i + r < WORDS)
+              *reinterpret_cast<float2*>(row + 8 * (8 * i + r) + 2 * j) = make_float2(o[nr][i][j][e], o[nr][i][j][2 + e]);
+      }
+  }
+  __syncthreads();
+  // ---------------- the warps' results joined
+  const bool lost = flags[0] != 0 || flags[1] != 0;
+  const float* red = reinterpret_cast<const float*>(smem);
+  for (int u = threadIdx.x; u < G::kRows * (HD / 2); u += G::THREADS) {
+    const int rr = u / (HD / 2), d = 2 * (u - rr * (HD / 2));
+    const int R = R0 + rr;
+    if (R >= n_rows) continue;
+    float mw[G::WARPS], mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < G::WARPS; ++w) {
+      mw[w] = red[(w * G::kRows + rr) * (HD + 2) + HD];
+      mx = fmaxf(mx, mw[w]);
+    }
+    float sum = 0.f, a0 = 0.f, a1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < G::WARPS; ++w) {
+      const float* row = red + (w * G::kRows + rr) * (HD + 2);
+      if (row[HD + 1] == 0.f) continue;   // no key seen
+      // a reference at -inf with a sum: every score was NaN, and so is the sum
+      const float f = mw[w] == -INFINITY ? 1.f : exp2f(mw[w] - mx);
+      sum += f * row[HD + 1];
+      a0 += f * row[d];
+      a1 += f * row[d + 1];
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    float lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);
+    a0 *= inv;
+    a1 *= inv;
+    if (lost) a0 = a1 = lse2 = __int_as_float(0x7FC00000);
+    const long t = rq.q0 + R / p.group;
+    const int h = g * p.group + R % p.group;
+    if (p.n_splits == 1) {
+      *reinterpret_cast<uint32_t*>(p.out + t * p.o_tok + h * p.o_head + d) =
+          (uint32_t)f32_to_bf16_any(a0) | ((uint32_t)f32_to_bf16_any(a1) << 16);
+      if (d == 0 && p.lse != nullptr) p.lse[t * p.H + h] = lse2 * 0.6931471805599453f;
+    } else {
+      const long at = ((long)sp * p.T + t) * p.H + h;
+      *reinterpret_cast<float2*>(p.part_o + at * HD + d) = make_float2(a0, a1);
+      if (d == 0) p.part_lse[at] = lse2;
+    }
+  }
+}
+
+// Joins the splits of one query: one warp per head. Grid (max_q, B).
+template <int HD>
+__global__ void __launch_bounds__(256)
+attn_kv4_merge_kernel(const __grid_constant__ AttnKv4Params p) {
+  pdl_begin();
+  const Kv4Req rq = kv4_request(p, blockIdx.y);
+  if (rq.skip || rq.bad || (int)blockIdx.x >= rq.n) return;
+  const long t = rq.q0 + blockIdx.x;
+  const int lane = threadIdx.x & 31;
+  // splits past every key the request's rows see wrote no partial of this row's tile: all wrote their lse
+  for (int h = threadIdx.x >> 5; h < p.H; h += blockDim.x >> 5) {
+    float mx = -INFINITY;
+    bool nan = false;
+    for (int s = lane; s < p.n_splits; s += 32) {
+      const float v = p.part_lse[((long)s * p.T + t) * p.H + h];
+      nan |= v != v;
+      mx = fmaxf(mx, v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    nan = __any_sync(0xffffffffu, nan);
+    float acc[(HD + 63) / 64][2];
+#pragma unroll
+    for (int i = 0; i < (HD + 63) / 64; ++i) acc[i][0] = acc[i][1] = 0.f;
+    float sum = 0.f;
+    if (mx != -INFINITY) {
+      for (int s = 0; s < p.n_splits; ++s) {
+        const long at = ((long)s * p.T + t) * p.H + h;
+        const float w = exp2f(p.part_lse[at] - mx);
+        if (w == 0.f) continue;
+        sum += w;
+        const float* po = p.part_o + at * HD;
+#pragma unroll
+        for (int i = 0; i < (HD + 63) / 64; ++i) {
+          const int d = 64 * i + 2 * lane;
+          if (d < HD) {
+            const float2 v = *reinterpret_cast<const float2*>(po + d);
+            acc[i][0] += w * v.x;
+            acc[i][1] += w * v.y;
+          }
+        }
+      }
+    }
+    const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
+    const float qnan = __int_as_float(0x7FC00000);
+#pragma unroll
+    for (int i = 0; i < (HD + 63) / 64; ++i) {
+      const int d = 64 * i + 2 * lane;
+      if (d < HD)
+        *reinterpret_cast<uint32_t*>(p.out + t * p.o_tok + h * p.o_head + d) =
+            (uint32_t)f32_to_bf16_any(nan ? qnan : acc[i][0] * inv) |
+            ((uint32_t)f32_to_bf16_any(nan ? qnan : acc[i][1] * inv) << 16);
+    }
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[t * p.H + h] = nan ? qnan : mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+}  // namespace dllm

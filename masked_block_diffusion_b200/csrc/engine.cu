@@ -32,6 +32,10 @@
 
 using namespace dllm;
 
+namespace dllm {
+cudaError_t kv4_set_wait_limit(unsigned long long ns);   // kv4.cu
+}
+
 namespace {
 
 // NVTX range for the duration of a scope: entry points and, when kernels are launched
@@ -1420,6 +1424,7 @@ int dllm_set_wait_limit(dllm_handle* h, long long ns) {
   const unsigned long long v = ns > 0 ? (unsigned long long)ns : kWaitLimitNs;
   CK(cudaStreamSynchronize(h->st));
   CK(cudaMemcpyToSymbol(g_wait_limit_ns, &v, sizeof(v)));
+  CK(kv4_set_wait_limit(v));
   return DLLM_OK;
 }
 

@@ -1,0 +1,270 @@
+"""Rotary positions and the paged 4-bit KV cache on torch tensors.
+
+``Rope`` is a rotation plan, ``rope`` rotates a tensor, ``KVCache4`` holds one layer's pages
+and appends to them, reads them back and attends to them. Each call checks its tensors,
+queues one or two kernels of libdllm.so on the current stream of the tensors' device
+(whichever device is current) and returns; it can be captured in a CUDA graph. The C ABI
+behind it (include/dllm.h) says what each call computes and how it treats padding, bad page
+ids and bad lengths.
+
+Tensors are those of the call's stream: as with any torch operation, the caller orders other
+streams' work on them.
+"""
+
+from __future__ import annotations
+
+import math
+from typing import Optional, Tuple
+
+import torch
+
+from . import binding
+
+_TYPES = {torch.float32: binding.DLLM_F32, torch.bfloat16: binding.DLLM_BF16}
+_LAYOUTS = {"half": binding.DLLM_ROPE_HALF, "interleaved": binding.DLLM_ROPE_INTERLEAVED}
+_SCALINGS = {"none": binding.DLLM_ROPE_NONE, "linear": binding.DLLM_ROPE_LINEAR, "ntk": binding.DLLM_ROPE_NTK,
+             "yarn": binding.DLLM_ROPE_YARN}
+
+
+class Rope:
+    """A rotation plan: which dims of a head turn, and how fast (dllm_rope_init).
+
+    layout: "half" pairs dims (i, i + rotary_dim / 2), "interleaved" pairs (2 i, 2 i + 1).
+    scaling for contexts beyond the trained one: "none", "linear", "ntk" or "yarn" with
+    `factor`; original_ctx, beta_fast and beta_slow are for "yarn".
+    """
+
+    def __init__(self, rotary_dim: int, layout: str = "half", theta: float = 10000.0, scaling: str = "none",
+                 factor: float = 1.0, original_ctx: float = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0):
+        if layout not in _LAYOUTS:
+            raise ValueError(f"layout {layout!r}: one of {sorted(_LAYOUTS)}")
+        if scaling not in _SCALINGS:
+            raise ValueError(f"scaling {scaling!r}: one of {sorted(_SCALINGS)}")
+        self.c = binding.dllm_rope_init(int(rotary_dim), _LAYOUTS[layout], float(theta), _SCALINGS[scaling],
+                                        float(factor), float(original_ctx), float(beta_fast), float(beta_slow))
+        self.rotary_dim, self.layout, self.magnitude = int(rotary_dim), layout, self.c.magnitude
+
+
+def _bad(name: str, why: str):
+    raise ValueError(f"{name}: {why}")
+
+
+def _heads(name: str, t: torch.Tensor, device, shape, dtypes) -> None:
+    """A [T][heads][dim] tensor whose last dimension is contiguous."""
+    if t.device != device:
+        _bad(name, f"on {t.device}, expected {device}")
+    if t.dtype not in dtypes:
+        _bad(name, f"{t.dtype}, expected one of {[str(d) for d in dtypes]}")
+    if t.dim() != 3 or tuple(t.shape) != tuple(shape):
+        _bad(name, f"shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        _bad(name, "the last dimension has to be contiguous")
+
+
+def _ints(name: str, t: torch.Tensor, device, n: int) -> None:
+    if t.device != device:
+        _bad(name, f"on {t.device}, expected {device}")
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        _bad(name, f"expected a contiguous int32 tensor of {n}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _table(t: torch.Tensor, device) -> None:
+    if t.device != device:
+        _bad("table", f"on {t.device}, expected {device}")
+    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1):
+        _bad("table", f"expected int32 [requests][pages] with contiguous rows, got {t.dtype} {tuple(t.shape)}")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _strides(t: torch.Tensor) -> Tuple[int, int]:
+    """Token and head strides; a dimension of one element has none that matters."""
+    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+
+
+def _no_grad(*tensors) -> None:
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise RuntimeError("these operations record no gradient: call them on detached tensors "
+                           "(rope(..., transposed=True) is the gradient of rope)")
+
+
+class _on:
+    """Makes `device` current for a launch and gives its current stream."""
+
+    def __init__(self, device: torch.device):
+        if device.type != "cuda":
+            raise ValueError(f"tensors on {device}: a CUDA device is needed")
+        self.index = device.index
+        self.guard = None
+
+    def __enter__(self) -> int:
+        if torch.cuda.current_device() != self.index:
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+        return torch.cuda.current_stream(self.index).cuda_stream
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def rope(x: torch.Tensor, pos: torch.Tensor, plan: Rope, out: Optional[torch.Tensor] = None,
+         out_dtype: Optional[torch.dtype] = None, transposed: bool = False) -> torch.Tensor:
+    """x [T][heads][head_dim] (fp32 or bf16, strided) rotated to positions pos (int32 [T]).
+
+    out: where the result goes (x itself rotates in place); without it a new contiguous tensor
+    of out_dtype (x's type by default). transposed: the transposed map, i.e. the gradient."""
+    if x.dim() != 3:
+        _bad("x", f"expected [T][heads][head_dim], got {tuple(x.shape)}")
+    _heads("x", x, x.device, x.shape, _TYPES)
+    _no_grad(x, out)
+    T, H, hd = x.shape
+    _ints("pos", pos, x.device, T)
+    if out is None:
+        dtype = out_dtype or x.dtype
+        if dtype not in _TYPES:
+            _bad("out_dtype", f"{dtype}, expected one of {[str(d) for d in _TYPES]}")
+        out = torch.empty((T, H, hd), dtype=dtype, device=x.device)
+    else:
+        _heads("out", out, x.device, x.shape, _TYPES)
+        if out_dtype is not None and out_dtype != out.dtype:
+            _bad("out", f"{out.dtype}, but out_dtype is {out_dtype}")
+    with _on(x.device) as stream:
+        binding.dllm_op_rope(plan.c, x.data_ptr(), _TYPES[x.dtype], *_strides(x), pos.data_ptr(), T, H, hd,
+                             out.data_ptr(), _TYPES[out.dtype], *_strides(out), 1 if transposed else 0,
+                             stream)
+    return out
+
+
+class KVCache4:
+    """One layer's pages of 4-bit keys and values, 0.5625 bytes per value.
+
+    codes uint8 [n_pages][2][n_kv_heads][page][head_dim / 2] and scales uint8
+    [n_pages][2][n_kv_heads][page][head_dim / 16], as include/dllm.h lays them out. Page tables
+    belong to the caller: int32 [requests][pages per request].
+    """
+
+    def __init__(self, n_pages: int, page: int, n_kv_heads: int, head_dim: int, device="cuda"):
+        if page not in (16, 32, 64, 128, 256):
+            _bad("page", f"{page}: 16, 32, 64, 128 or 256 positions")
+        if head_dim not in (64, 128, 176):
+            _bad("head_dim", f"{head_dim}: 64, 128 or 176")
+        if n_pages < 1 or n_kv_heads < 1:
+            _bad("n_pages, n_kv_heads", "at least 1 each")
+        shape = (n_pages, 2, n_kv_heads, page)
+        self._init(torch.zeros((*shape, head_dim // 2), dtype=torch.uint8, device=device),
+                   torch.zeros((*shape, head_dim // 16), dtype=torch.uint8, device=device))
+
+    @classmethod
+    def from_tensors(cls, codes: torch.Tensor, scales: torch.Tensor) -> "KVCache4":
+        """A cache over the caller's own arrays."""
+        self = cls.__new__(cls)
+        self._init(codes, scales)
+        return self
+
+    def _init(self, codes, scales):
+        for name, t in (("codes", codes), ("scales", scales)):
+            if t.dtype != torch.uint8 or t.dim() != 5 or not t.is_contiguous():
+                _bad(name, "expected a contiguous uint8 tensor of 5 dimensions")
+            if t.data_ptr() % 16:
+                _bad(name, "has to lie on a 16-byte boundary")
+        if codes.device != scales.device or codes.shape[:4] != scales.shape[:4] or codes.shape[1] != 2 \
+                or codes.shape[4] != 8 * scales.shape[4]:
+            _bad("codes, scales", f"{tuple(codes.shape)} and {tuple(scales.shape)} do not belong together")
+        self.codes, self.scales, self.device = codes, scales, codes.device
+        self.n_pages, _, self.n_kv_heads, self.page = codes.shape[:4]
+        self.head_dim = 2 * codes.shape[4]
+        self.c = binding.dllm_kv4(codes.data_ptr(), scales.data_ptr(), self.n_pages, self.page, self.n_kv_heads,
+                                  self.head_dim)
+        if self.device.type != "cuda":
+            _bad("codes, scales", f"on {self.device}: a CUDA device is needed")
+        # the library's own check of the sizes
+        binding.dllm_op_attn_kv4_workspace(self.c, 0, 0, 0, 0, self.n_kv_heads)
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, req: torch.Tensor, pos: torch.Tensor, table: torch.Tensor,
+               rope: Optional[Rope] = None, rope_pos: Optional[torch.Tensor] = None) -> None:
+        """Writes k, v [T][n_kv_heads][head_dim] (one type, fp32 or bf16, strided) to positions pos of
+        table rows req (int32 [T]; req < 0: padding), k rotated by `rope` to rope_pos (pos by default)."""
+        T = k.shape[0]
+        shape = (T, self.n_kv_heads, self.head_dim)
+        _heads("k", k, self.device, shape, _TYPES)
+        _heads("v", v, self.device, shape, (k.dtype,))
+        _no_grad(k, v)
+        _ints("req", req, self.device, T)
+        _ints("pos", pos, self.device, T)
+        _table(table, self.device)
+        if rope_pos is not None:
+            _ints("rope_pos", rope_pos, self.device, T)
+        with _on(self.device) as stream:
+            binding.dllm_op_append_kv4(self.c, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), _TYPES[k.dtype], req.data_ptr(), pos.data_ptr(),
+                                       None if rope_pos is None else rope_pos.data_ptr(), T, table.data_ptr(),
+                                       table.shape[0], _row_stride(table), None if rope is None else rope.c, stream)
+
+    def read(self, req: torch.Tensor, pos: torch.Tensor, table: torch.Tensor, k_out: Optional[torch.Tensor] = None,
+             v_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Positions pos of table rows req as bf16 (k, v), each [T][n_kv_heads][head_dim]. Rows of padding
+        (req < 0) are left as they were in k_out and v_out, and are zero in outputs made here."""
+        T = req.shape[0]
+        shape = (T, self.n_kv_heads, self.head_dim)
+        _ints("req", req, self.device, T)
+        _ints("pos", pos, self.device, T)
+        _table(table, self.device)
+        outs = []
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is None:
+                t = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+            else:
+                _heads(name, t, self.device, shape, (torch.bfloat16,))
+                if not t.is_contiguous():
+                    _bad(name, "has to be contiguous")
+            outs.append(t)
+        with _on(self.device) as stream:
+            binding.dllm_op_read_kv4(self.c, req.data_ptr(), pos.data_ptr(), T, table.data_ptr(), table.shape[0],
+                                     _row_stride(table), outs[0].data_ptr(), outs[1].data_ptr(), stream)
+        return outs[0], outs[1]
+
+    def attend(self, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor, max_q: int,
+               max_kv: int, causal: bool = False, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+               return_lse: bool = False, workspace: Optional[torch.Tensor] = None):
+        """Attention of a batch's queries over the cache (dllm_op_attn_kv4).
+
+        q bf16 [T][heads][head_dim]; request b's queries are rows q_start[b] .. q_start[b + 1] - 1 and
+        it sees positions below kv_len[b] of table row b; causal: its queries are the last of
+        those. max_q, max_kv: bounds on a request's queries and keys. scale: 1 / sqrt(head_dim)
+        by default. workspace: a uint8 tensor of workspace_bytes(...) for callers that allocate
+        nothing here. Returns out (bf16, q's shape), with return_lse (out, lse fp32 [T][heads])."""
+        if q.dim() != 3:
+            _bad("q", f"expected [T][heads][head_dim], got {tuple(q.shape)}")
+        T, H, hd = q.shape
+        _heads("q", q, self.device, (T, H, self.head_dim), (torch.bfloat16,))
+        _no_grad(q)
+        B = kv_len.shape[0]
+        _ints("kv_len", kv_len, self.device, B)
+        _ints("q_start", q_start, self.device, B + 1)
+        _table(table, self.device)
+        if table.shape[0] < B:
+            _bad("table", f"{table.shape[0]} rows for {B} requests")
+        if out is None:
+            out = torch.empty((T, H, hd), dtype=torch.bfloat16, device=self.device)
+        else:
+            _heads("out", out, self.device, (T, H, hd), (torch.bfloat16,))
+        lse = torch.empty((T, H), dtype=torch.float32, device=self.device) if return_lse else None
+        need = self.workspace_bytes(B, T, max_q, max_kv, H)
+        if workspace is None:
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        elif workspace.device != self.device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            _bad("workspace", "expected a contiguous uint8 tensor on the cache's device")
+        with _on(self.device) as stream:
+            binding.dllm_op_attn_kv4(self.c, q.data_ptr(), *_strides(q), out.data_ptr(), *_strides(out), None if lse is None else lse.data_ptr(), q_start.data_ptr(),
+                                     kv_len.data_ptr(), B, T, max_q, max_kv, H, table.data_ptr(), _row_stride(table),
+                                     1 if causal else 0, 1.0 / math.sqrt(hd) if scale is None else scale,
+                                     None if workspace is None else workspace.data_ptr(),
+                                     0 if workspace is None else workspace.numel(), stream)
+        return (out, lse) if return_lse else out
+
+    def workspace_bytes(self, B: int, T: int, max_q: int, max_kv: int, heads: int) -> int:
+        """Bytes of workspace that attend() needs for these sizes."""
+        return binding.dllm_op_attn_kv4_workspace(self.c, B, T, max_q, max_kv, heads)
