@@ -20,7 +20,8 @@ COMMON = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompi
 # the library's translation units, compiled side by side, and the headers each one reads
 UNITS = {
     "engine": ["attention.cuh", "attention_tc.cuh", "common.cuh", "gemm_tc.cuh", "kernels.cuh"],
-    "kv4": ["attention.cuh", "attention_tc.cuh", "common.cuh", "attention_kv4.cuh", "kv4.cuh", "rope.cuh"],
+    "kv4": ["attention.cuh", "attention_tc.cuh", "common.cuh", "attention_kv4.cuh", "attention_kv4_tc.cuh", "kv4.cuh",
+            "rope.cuh"],
 }
 OBJ = os.path.join(PKG, "_build")
 

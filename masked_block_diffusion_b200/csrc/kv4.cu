@@ -8,6 +8,7 @@
 #include <cmath>
 
 #include "attention_kv4.cuh"
+#include "attention_kv4_tc.cuh"
 #include "kv4.cuh"
 #include "rope.cuh"
 
@@ -107,19 +108,21 @@ bool addr_ok(const int32_t* req, const int32_t* pos, const int32_t* table, int n
 // ---- attention: how a call is cut up
 
 struct AttnPlan {
-  int tiles, n_splits, chunk, nr;
+  int tiles, n_splits, chunk;
+  int nr;   // 8-row columns of the few-row kernel; 0: the tensor-core kernel
 };
 
-// Query rows per block of the few-row kernel: 8 where the request's rows fit, else 16.
+// Query rows per block: 8 or 16 of the few-row kernel, else 256 of the tensor-core kernel.
 AttnPlan attn_plan(int B, int max_q, int max_kv, int group, int Hkv) {
   AttnPlan a;
   const long rows = (long)max_q * group;
-  a.nr = rows <= 8 ? 1 : 2;
-  a.tiles = ceil_div(rows, 8 * a.nr);
+  a.nr = rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
+  a.tiles = ceil_div(rows, a.nr ? 8 * a.nr : 256);
   // Keys are split until the blocks fill the SMs' slots, but no split has fewer than 128 keys.
-  const long slots = kSMs * (a.nr == 1 ? 3 : 2);
+  const long slots = kSMs * (a.nr == 1 ? 3 : a.nr == 2 ? 2 : 1);
   const long blocks = (long)B * Hkv * a.tiles;
-  const long want = std::max(1L, std::min((slots + blocks - 1) / blocks, (max_kv + 127L) / 128));
+  const long fill = a.nr ? (slots + blocks - 1) / blocks : slots / blocks;
+  const long want = std::max(1L, std::min(fill, (max_kv + 127L) / 128));
   a.chunk = std::max(64, ceil_div(ceil_div(max_kv, want), 64) * 64);
   a.n_splits = std::max(1, ceil_div(max_kv, a.chunk));
   return a;
@@ -148,8 +151,17 @@ cudaError_t run_few(cudaStream_t st, const AttnPlan& a, const AttnKv4Params& p) 
 }
 
 template <int HD>
+cudaError_t run_tc(cudaStream_t st, const AttnPlan& a, const AttnKv4Params& p) {
+  using G = AttnKv4TcCfg<HD>;
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(attn_kv4_tc_kernel<HD>),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, G::kTotal);
+  if (e != cudaSuccess) return e;
+  return launch(st, attn_kv4_tc_kernel<HD>, dim3(a.tiles, a.n_splits, p.c.Hkv * p.B), G::THREADS, G::kTotal, p);
+}
+
+template <int HD>
 cudaError_t run_attn(cudaStream_t st, const AttnPlan& a, const AttnKv4Params& p) {
-  cudaError_t e = a.nr == 1 ? run_few<HD, 1>(st, a, p) : run_few<HD, 2>(st, a, p);
+  cudaError_t e = a.nr == 1 ? run_few<HD, 1>(st, a, p) : a.nr == 2 ? run_few<HD, 2>(st, a, p) : run_tc<HD>(st, a, p);
   if (e == cudaSuccess && a.n_splits > 1)
     e = launch(st, attn_kv4_merge_kernel<HD>, dim3(p.max_q, p.B), 256, 0, p);
   return e;
@@ -291,7 +303,8 @@ int dllm_op_attn_kv4(const dllm_kv4* cache, const uint16_t* q, long long q_token
     return DLLM_E_INVAL;
   const int group = H / cache->n_kv_heads;
   const AttnPlan a = attn_plan(B, max_q, max_kv, group, cache->n_kv_heads);
-  if ((long)cache->n_kv_heads * a.tiles > 65535) return DLLM_E_INVAL;
+  if ((a.nr ? (long)cache->n_kv_heads * a.tiles : (long)cache->n_kv_heads * B) > 65535 || a.n_splits > 65535)
+    return DLLM_E_INVAL;
   if (attn_workspace(a, T, H, cache->head_dim) > (workspace ? workspace_bytes : 0)) return DLLM_E_INVAL;
   AttnKv4Params p;
   p.c = cache_of(cache);
