@@ -8,18 +8,27 @@
 // products on the tensor pipe.
 //
 // Roles (512 threads):
-//   warp 0       TMEM; lane 0 issues the products: S_t = Q_t K^T (bf16) into tile t's S columns,
-//                O_t += P_t V (fp16) with P_t read from TMEM, where the softmax wrote it over S_t;
-//   warp 1       copies packed keys page by page into a ring (bulk copies, one lane per piece);
+//   warps 0, 1   each issues one tile's products (warp 0 holds the TMEM allocation): S_t = Q_t K^T
+//                (bf16) into tile t's S columns, and O_t += P_t V (fp16) with P_t read from
+//                TMEM. A wait and an issue cost such a warp some 200 cycles each among the busy
+//                warps of its scheduler, so one warp for both tiles was the bottleneck (2450
+//                cycles per 64 keys at head_dim 64). S_t(j + 1) goes out as soon as the
+//                softmax has read S_t(j) into registers, so a tile's next scores are ready when
+//                its softmax is (with P_t written over S_t instead, S_t(j + 1) has to wait for
+//                P_t V(j), and each tile's chain of product, softmax and product bounded the
+//                kernel: 251 us for 16 canvases);
 //   warps 4..7   softmax of tile 0, warps 8..11 of tile 1: one row per thread (TMEM lane), 64
 //                scores in registers, lazy reference as in attention_kv4.cuh; O is rescaled in
 //                TMEM when the reference moves (rare), and read and written out at the end;
-//   warps 12..15 unpack: K to bf16 and V to fp16, both exact, as 64-dim atoms of 128-byte
-//                rows with the 128-byte swizzle (K's rows are keys, K-major; V's are the same
-//                rows read as the MN-major operand). Eight consecutive lanes write 4 groups
-//                of 2 adjacent keys: 8 different 16-byte columns, no bank conflict.
-//   warps 2, 3   only help to load Q.
-// TMEM: S_t at 64 t, O_t at 128 + HD t: 480 of 512 columns at head_dim 176.
+//   the others   (2, 3, 12..15) unpack: K to bf16 and V to fp16, both exact, as 64-dim atoms of
+//                128-byte rows with the 128-byte swizzle (K's rows are keys, K-major; V's are the
+//                same rows read as the MN-major operand). Eight consecutive lanes write 4 groups
+//                of 2 adjacent keys: 8 different 16-byte columns, no bank conflict. The packed
+//                bytes come straight into registers, a block of keys ahead, and the page ids two
+//                blocks ahead.
+// TMEM: S_t at 64 t, then P, then O_t. At head_dim 176 there is room for one P (32 columns) beside
+// 2 x 64 columns of S and 2 x 176 of O: the tiles use it in turn, each writing once the other's
+// product has read it. Smaller heads have a P for each tile.
 // Every wait is bounded, as in gemm_tc.cuh; a block that gives one up writes NaN.
 #pragma once
 
@@ -32,43 +41,82 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32_bmn(int M, int N) {
   return (1u << 4) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// True in one lane of a converged warp, always the same one. The warp that issues the products
+// runs its loop as a whole and lets the elected lane issue: descriptors, addresses and loop
+// state are then the same in every lane, and stay in uniform registers, which is where the
+// tensor instructions take them from. (In a branch that only lane 0 enters, each product cost
+// about 150 cycles to issue, more than it took to run.)
+DLLM_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
 template <int HD>
 struct AttnKv4TcCfg {
   static constexpr int BK = 64;
   static constexpr int ATOMS = (HD + 63) / 64;
-  static constexpr int STAGES = 2;                       // unpacked K and V
-  static constexpr int RAW = HD == 176 ? 2 : 4;          // packed stages
+  static constexpr int KST = 3, VST = 2;                 // unpacked stages of K and of V
   static constexpr int kQTile = ATOMS * 128 * 128;
   static constexpr int kAtom = BK * 128;
   static constexpr int kKV = ATOMS * kAtom;
-  static constexpr int kCodes = BK * HD / 2;
-  static constexpr int kScales = BK * HD / 16;
-  static constexpr int kRawStage = 2 * (kCodes + kScales);
   static constexpr int kOffK = 2 * kQTile;
-  static constexpr int kOffV = kOffK + STAGES * kKV;
-  static constexpr int kOffRaw = kOffV + STAGES * kKV;
-  static constexpr int kOffBar = kOffRaw + RAW * kRawStage;
+  static constexpr int kOffV = kOffK + KST * kKV;
+  static constexpr int kOffBar = kOffV + VST * kKV;
   static constexpr int kTotal = kOffBar + 256 + 1024;
-  static constexpr int kOCol = 2 * BK;
+  static constexpr bool kOneP = 2 * BK + 2 * (BK / 2) + 2 * HD > 512;
+  static constexpr int kPCol = 2 * BK;
+  static constexpr int kOCol = kPCol + (kOneP ? 1 : 2) * (BK / 2);
   static constexpr int kTmemCols = 512;
   static constexpr int THREADS = 512;
+  // An unpacking warp has OCT groups of 8 keys of one atom of K and of V; UNPACK warps cover a block.
+  static constexpr int OCT = ATOMS == 1 ? 2 : 4;
+  static constexpr int UNPACK = ATOMS * 8 / OCT;
+  static_assert(UNPACK <= 6, "warps 2, 3, 12..15");
   static_assert(kOCol + 2 * HD <= kTmemCols, "TMEM");
   static_assert(kTotal <= 232448, "shared memory");
   static_assert(kOffBar % 16 == 0, "barriers");
 };
 
+// Two fp32 operations in one instruction.
+DLLM_DEV uint64_t pack_f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+DLLM_DEV void unpack_f32x2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+DLLM_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+DLLM_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Tile t's softmax: thread (warp w, lane) owns row 32 (w % 4) + lane of the tile.
 template <int HD>
 DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_t tmem_base, uint64_t* s_full,
-                               uint64_t* p_full, uint64_t* o_final, volatile int* flags, int t, int R0, int g, int sp,
-                               int ks, int ke, int nblk) {
+                               uint64_t* s_read, uint64_t* p_full, uint64_t* pv_done, volatile int* flags,
+                               int t, int nt, int R0, int g, int sp, int ks, int ke, int nblk) {
   using G = AttnKv4TcCfg<HD>;
   constexpr int BK = G::BK;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = 32 * (warp & 3) + lane;
   const uint32_t lane_base = tmem_base + ((uint32_t)(32 * (warp & 3)) << 16);
   const uint32_t s_col = lane_base + t * BK;
+  const uint32_t p_col = lane_base + G::kPCol + (G::kOneP ? 0 : t * (BK / 2));
   const uint32_t o_col = lane_base + G::kOCol + t * HD;
+  // P's columns are free once the last product that read them is done: this tile's of the block before, or
+  // where the tiles share them the other tile's last one (which is later than this tile's)
+  const int before = G::kOneP && nt == 2 ? t ^ 1 : t;
+  const int lag = before < t ? 0 : 1;
   const int R = R0 + 128 * t + row;
   const bool real = R < rq.n * p.group;
   const int lim = real ? min(ke, kv4_row_limit(p, rq, R / p.group)) : ke;
@@ -79,6 +127,9 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_
     tc_fence_after();
     float s[BK];
     tmem_ld64(s_col, s);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s_read[t]);
     const int seen = lim - (ks + j * BK);
     if (seen < BK) {
 #pragma unroll
@@ -91,7 +142,9 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_
     } else {
       const bool need = mx > m + (kKv4Low + 8.f);
       if (__any_sync(0xffffffffu, need)) {
-        // tile t's O is stable here: S_t(j) was issued only after P_t V(j - 1) completed
+        // O is stable once the product of the block before is done
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[t], (j - 1) & 1, flags))) { ok = false; break; }
+        tc_fence_after();
         const float mn = need ? mx - kKv4Low : m;
         const float f = need ? exp2f(m - mn) : 1.0f;
 #pragma unroll 1
@@ -108,21 +161,32 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_
     }
     const float mb = m == -INFINITY ? 0.f : m;
     uint32_t pk[BK / 2];
+    const uint64_t sc2 = pack_f32x2(p.scale_log2, p.scale_log2), mb2 = pack_f32x2(-mb, -mb);
+    uint64_t sum[4] = {0, 0, 0, 0};   // pairs of fp32 sums
 #pragma unroll
     for (int c = 0; c < BK; c += 2) {
-      s[c] = ex2_approx(fmaf(s[c], p.scale_log2, -mb));
-      s[c + 1] = ex2_approx(fmaf(s[c + 1], p.scale_log2, -mb));
-      const __half2 h = __floats2half2_rn(s[c], s[c + 1]);
+      float a, b;
+      unpack_f32x2(fma_f32x2(pack_f32x2(s[c], s[c + 1]), sc2, mb2), a, b);
+      a = ex2_approx(a);
+      b = ex2_approx(b);
+      sum[(c / 2) & 3] = add_f32x2(sum[(c / 2) & 3], pack_f32x2(a, b));
+      const __half2 h = __floats2half2_rn(a, b);
       pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    tmem_st32_nowait(s_col, pk);
-    l += tree_sum<BK>(s);
+    if (j >= lag) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[before], (j - lag) & 1, flags))) { ok = false; break; }
+      tc_fence_after();
+    }
+    tmem_st32_nowait(p_col, pk);
+    float l0, l1;
+    unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), l0, l1);
+    l += l0 + l1;
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&p_full[t]);
   }
-  if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_final, 0, flags));
+  if (ok && nblk > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], (nblk - 1) & 1, flags));
   if (!ok) flags[0] = 1;
   tc_fence_after();
   const bool lost = flags[0] != 0 || flags[1] != 0;
@@ -170,26 +234,23 @@ template <int HD>
 __global__ void __launch_bounds__(AttnKv4TcCfg<HD>::THREADS, 1)
 attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
   using G = AttnKv4TcCfg<HD>;
-  constexpr int BK = G::BK, AT = G::ATOMS, ST = G::STAGES;
+  constexpr int BK = G::BK, AT = G::ATOMS, KST = G::KST, VST = G::VST;
   constexpr uint32_t kIdQK = idesc_bf16_f32(128, BK);
   constexpr uint32_t kIdPV = idesc_f16_f32_bmn(128, HD);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem + G::kOffK;
   uint8_t* sV = smem + G::kOffV;
-  uint8_t* sR = smem + G::kOffRaw;
-  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);
-  uint64_t* raw_empty = raw_full + G::RAW;
-  uint64_t* k_full = raw_empty + G::RAW;
-  uint64_t* k_empty = k_full + ST;
-  uint64_t* v_full = k_empty + ST;
-  uint64_t* v_empty = v_full + ST;
-  uint64_t* s_full = v_empty + ST;   // [2]: S_t(j) is in its columns
-  uint64_t* p_full = s_full + 2;     // [2]: P_t(j) is written over it
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);
+  uint64_t* k_empty = k_full + KST;
+  uint64_t* v_full = k_empty + KST;
+  uint64_t* v_empty = v_full + VST;
+  uint64_t* s_full = v_empty + VST;  // [2]: S_t(j) is in its columns
+  uint64_t* s_read = s_full + 2;     // [2]: the softmax has it in registers
+  uint64_t* p_full = s_read + 2;     // [2]: P_t(j) is in its columns
   uint64_t* pv_done = p_full + 2;    // [2]: P_t V(j) completed
-  uint64_t* o_final = pv_done + 2;
-  uint64_t* drain = o_final + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* drain = pv_done + 2;     // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [0] abort, [1] a page that is none
 
   pdl_wait();
@@ -211,23 +272,21 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < G::RAW; ++s) {
-      mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], 4);
+    for (int s = 0; s < KST; ++s) {
+      mbar_init(&k_full[s], G::UNPACK);
+      mbar_init(&k_empty[s], nt);
     }
-    for (int s = 0; s < ST; ++s) {
-      mbar_init(&k_full[s], 4);
-      mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], 4);
-      mbar_init(&v_empty[s], 1);
+    for (int s = 0; s < VST; ++s) {
+      mbar_init(&v_full[s], G::UNPACK);
+      mbar_init(&v_empty[s], nt);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
+      mbar_init(&s_read[t], 4);
       mbar_init(&p_full[t], 4);
       mbar_init(&pv_done[t], 1);
+      mbar_init(&drain[t], 1);
     }
-    mbar_init(o_final, 1);
-    mbar_init(drain, 1);
     flags[0] = flags[1] = 0;
     fence_mbar_init();
   }
@@ -251,148 +310,173 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
   pdl_trigger();   // after the TMEM allocation
   const uint32_t tmem_base = *tmem_slot;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- MMA issuer
-      bool ok = true;
-      auto issue_s = [&](int t, int j) -> bool {
-        const int st = j % ST;
-        if (!mbar_wait(&k_full[st], (j / ST) & 1, flags)) return false;
+  if (warp < 2) {
+    if (warp < nt) {
+      // ---------------- MMA issuer of tile `warp`: the warp waits as one, an elected lane issues
+      const int t = __shfl_sync(0xffffffffu, warp, 0);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
+      const uint32_t s_col = tm + t * BK, p_col = tm + G::kPCol + (G::kOneP ? 0 : t * (BK / 2)), o_col = tm + G::kOCol + t * HD;
+      const uint64_t qd = sdesc_k_sw128(smem_u32(smem + t * G::kQTile));
+      const uint64_t kd0 = sdesc_k_sw128(smem_u32(sK)), vd0 = sdesc_mn_sw128(smem_u32(sV), G::kAtom);
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, flags));
+      };
+      int kst = 0, vst = 0;        // stages and their parities
+      uint32_t kph = 0, vph = 0;
+      auto issue_s = [&]() -> bool {
+        if (!wait(&k_full[kst], kph)) return false;
         tc_fence_after();
-        const uint32_t d = tmem_base + t * BK;
-        const uint32_t qb = smem_u32(smem + t * G::kQTile), kb = smem_u32(sK + st * G::kKV);
+        if (elect_one()) {
+          const uint64_t kd = kd0 + kst * (G::kKV >> 4);   // descriptors count 16-byte units
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k)
-          umma_bf16(d, sdesc_k_sw128(qb + (k >> 2) * 128 * 128 + (k & 3) * 32),
-                    sdesc_k_sw128(kb + (k >> 2) * G::kAtom + (k & 3) * 32), kIdQK, k != 0);
-        umma_commit(&s_full[t]);
-        if (t == nt - 1) umma_commit(&k_empty[st]);
+          for (int k = 0; k < HD / 16; ++k)
+            umma_bf16(s_col, qd + (((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4),
+                      kd + (((k >> 2) * G::kAtom + (k & 3) * 32) >> 4), kIdQK, k != 0);
+          umma_commit(&s_full[t]);
+          umma_commit(&k_empty[kst]);
+        }
+        __syncwarp();
+        if (++kst == KST) { kst = 0; kph ^= 1; }
         return true;
       };
-      auto issue_pv = [&](int t, int j) -> bool {
-        const int st = j % ST;
-        if (!mbar_wait(&v_full[st], (j / ST) & 1, flags)) return false;
-        if (!mbar_wait(&p_full[t], j & 1, flags)) return false;
+      bool ok = nblk == 0 || issue_s();
+      for (int j = 0; j < nblk && ok; ++j) {
+        if (j + 1 < nblk && !(wait(&s_read[t], j & 1) && issue_s())) { ok = false; break; }
+        if (!wait(&v_full[vst], vph) || !wait(&p_full[t], j & 1)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t vb = smem_u32(sV + st * G::kKV);
+        if (elect_one()) {
+          const uint64_t vd = vd0 + vst * (G::kKV >> 4);
 #pragma unroll
-        for (int k = 0; k < BK / 16; ++k)
-          umma_bf16_ts(tmem_base + G::kOCol + t * HD, tmem_base + t * BK + k * 8,
-                       sdesc_mn_sw128(vb + k * 16 * 128, G::kAtom), kIdPV, (j | k) != 0);
-        umma_commit(&pv_done[t]);
-        if (t == nt - 1) umma_commit(&v_empty[st]);
-        return true;
-      };
-      for (int t = 0; t < nt && ok && nblk > 0; ++t) ok = issue_s(t, 0);
-      for (int j = 0; j < nblk && ok; ++j)
-        for (int t = 0; t < nt && ok; ++t) {
-          ok = issue_pv(t, j);
-          // S_t(j + 1) goes over the columns that P_t V(j) reads
-          if (ok && j + 1 < nblk) ok = mbar_wait(&pv_done[t], j & 1, flags) && issue_s(t, j + 1);
+          for (int k = 0; k < BK / 16; ++k)
+            umma_bf16_ts(o_col, p_col + k * 8, vd + ((k * 16 * 128) >> 4), kIdPV, (j | k) != 0);
+          umma_commit(&pv_done[t]);
+          umma_commit(&v_empty[vst]);
         }
-      if (ok) umma_commit(o_final);
-      else flags[0] = 1;
-      umma_commit(drain);
-      mbar_drain(drain, 0);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ---------------- packed keys: lane i copies piece i of a block (a page's share of it)
-    const int shift = min(p.c.page_shift, 6);
-    const int pieces = BK >> shift, keys = 1 << shift;
-    const uint32_t codes = keys * HD / 2, scales = keys * HD / 16;
-    const int* trow = p.table + (long)b * p.stride;
-    bool ok = true;
-    int j = 0;
-    for (; j < nblk; ++j) {
-      const int t = ks + j * BK + lane * keys;
-      int id = -1;
-      if (lane < pieces && t < ke) {
-        id = trow[t >> p.c.page_shift];
-        if (id < 0 || id >= p.c.n_pages) {
-          id = -1;
-          flags[1] = 1;
-        }
+        __syncwarp();
+        if (++vst == VST) { vst = 0; vph ^= 1; }
       }
-      const uint32_t n = __popc(__ballot_sync(0xffffffffu, id >= 0));
-      const int st = j % G::RAW;
-      if (!mbar_wait(&raw_empty[st], ((j / G::RAW) & 1) ^ 1, flags)) ok = false;
-      if (!__all_sync(0xffffffffu, ok)) break;
-      if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], n * 2 * (codes + scales));
+      if (!ok) flags[0] = 1;
+      if (elect_one()) umma_commit(&drain[t]);
       __syncwarp();
-      if (id >= 0) {
-        const int off = t & ((1 << p.c.page_shift) - 1);
+      mbar_drain(&drain[t], 0);
+      __syncwarp();
+    }
+  } else if (warp < 4 || warp >= 12) {
+    // ---------------- unpacking
+    const int u = warp < 4 ? warp - 2 : warp >= 14 ? warp - 12 : warp - 8;   // 2, 3, 14, 15, 12, 13
+    constexpr int OCT = G::OCT;
+    const int a = u / (8 / OCT);                                 // the warp's atom
+    const int grp = lane & 3, gg = 4 * a + grp;
+    const int key0 = 8 * OCT * (u % (8 / OCT)) + (lane >> 2);    // the thread's keys of a block: key0 + 8 i, i < OCT
+    const int* trow = p.table + (long)b * p.stride;
+    const int mask = (1 << p.c.page_shift) - 1;
+    const bool mine = u < G::UNPACK;
+    // page id of key `key` of block j; -1 past the end, and for an id that is no page
+    auto page_of = [&](int j, int key) -> int {
+      const int t = ks + j * BK + key;
+      if (j >= nblk || t >= ke) return -1;
+      const int id = trow[t >> p.c.page_shift];
+      if (id >= 0 && id < p.c.n_pages) return id;
+      flags[1] = 1;
+      return -1;
+    };
+    const long v_rows = (long)p.c.Hkv << p.c.page_shift, page_rows = 2 * v_rows;
+    const long v_code = v_rows * (HD / 2), v_scale = v_rows * (HD / 16);
+    const int head_row = g << p.c.page_shift;
+    uint2 code[2][OCT];
+    uint32_t byte[2][OCT];
+    int id[OCT / 2];   // keys 16 m .. 16 m + 15 are in one page
+    // the next block's bytes: keys that do not exist get scale 0, so become 0
+    auto fetch = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < OCT; ++i) {
+        const bool have = id[i / 2] >= 0 && ks + j * BK + key0 + 8 * i < ke && 16 * gg < HD;
+        const long r = max(id[i / 2], 0) * page_rows + (head_row + ((ks + j * BK + key0 + 8 * i) & mask));
+        const uint8_t* pc = p.c.codes + r * (HD / 2) + 8 * gg;
+        const uint8_t* ps = p.c.scales + r * (HD / 16) + gg;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          const long r = kv4_row(p.c, id, kv, g, off);
-          uint8_t* d = sR + st * G::kRawStage + kv * (G::kCodes + G::kScales);
-          bulk_load(d + lane * codes, p.c.codes + r * (HD / 2), codes, &raw_full[st]);
-          bulk_load(d + G::kCodes + lane * scales, p.c.scales + r * (HD / 16), scales, &raw_full[st]);
+          code[kv][i] = make_uint2(0, 0);
+          byte[kv][i] = 0;
+          if (have) {
+            code[kv][i] = *reinterpret_cast<const uint2*>(pc + (kv ? v_code : 0));
+            byte[kv][i] = ps[kv ? v_scale : 0];
+          }
         }
       }
-    }
-    if (!__all_sync(0xffffffffu, ok)) flags[0] = 1;
-    // the copies already issued land before the block's shared memory goes away
-    for (int i = max(0, j - G::RAW); i < j; ++i) mbar_drain(&raw_full[i % G::RAW], (i / G::RAW) & 1);
-  } else if (warp >= 12) {
-    // ---------------- unpacking: a warp's turn is 8 keys of one 64-dim atom
-    const int w = warp - 12;
-    const int grp = lane & 3, k8 = lane >> 2;
+    };
+    auto pages = [&](int j) {
+#pragma unroll
+      for (int m = 0; m < OCT / 2; ++m) id[m] = page_of(j, key0 - (lane >> 2) + 16 * m);
+    };
+    const uint32_t at0 = a * G::kAtom + key0 * 128 + (((2 * grp) ^ (key0 & 7)) << 4);
     bool ok = true;
-    for (int j = 0; j < nblk && ok; ++j) {
-      const int rs = j % G::RAW, st = j % ST;
-      const int left = ke - (ks + j * BK);   // keys past the end become 0, whatever their bytes hold
-      if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[rs], (j / G::RAW) & 1, flags))) { ok = false; break; }
+    if (mine) {
+      pages(0);
+      fetch(0);
+      pages(1);
+    }
+    for (int j = 0; j < nblk && ok && mine; ++j) {
+      // this block's bytes have had a block's time to arrive; all loads of the next one are issued
+      // together before any is waited for again
+      uint2 now[2][OCT];
+      uint32_t scale[2][OCT];
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int i = 0; i < OCT; ++i) {
+          now[kv][i] = code[kv][i];
+          scale[kv][i] = byte[kv][i];
+          asm volatile("" : "+r"(now[kv][i].x), "+r"(now[kv][i].y), "+r"(scale[kv][i]));
+        }
+      fetch(j + 1);
+      pages(j + 2);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        uint64_t* empty = kv ? v_empty : k_empty;
-        uint64_t* full = kv ? v_full : k_full;
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ((j / ST) & 1) ^ 1, flags))) { ok = false; break; }
-        const uint8_t* rc = sR + rs * G::kRawStage + kv * (G::kCodes + G::kScales);
-        const uint8_t* rsc = rc + G::kCodes;
-        uint8_t* dst = (kv ? sV : sK) + st * G::kKV;
+        const int n = kv ? VST : KST, st = j % n;
+        if (!__all_sync(0xffffffffu, mbar_wait(&(kv ? v_empty : k_empty)[st], ((j / n) & 1) ^ 1, flags))) {
+          ok = false;
+          break;
+        }
+        uint8_t* dst = (kv ? sV : sK) + st * G::kKV + at0;
+        uint8_t* dst2 = (kv ? sV : sK) + st * G::kKV + (at0 ^ 16);
+        if (16 * gg < HD) {
 #pragma unroll
-        for (int i = 0; i < 2 * AT; ++i) {
-          const int key = 8 * (w + 4 * (i & 1)) + k8, a = i >> 1;
-          const int gg = 4 * a + grp;
-          if (16 * gg < HD) {
-            const uint2 c = *reinterpret_cast<const uint2*>(rc + key * (HD / 2) + 8 * gg);
-            const uint32_t byte = key < left ? rsc[key * (HD / 16) + gg] : 0;
+          for (int i = 0; i < OCT; ++i) {
+            const uint2 c = now[kv][i];
+            const uint32_t y = scale[kv][i];
             uint32_t o[8];
             if (kv == 0) {
-              const __nv_bfloat162 s = kv4_scale_bf16x2(byte);
-              const __nv_bfloat162 n = __hmul2(s, __float2bfloat162_rn(-24.f));
+              const __nv_bfloat162 s = kv4_scale_bf16x2(y);
+              const __nv_bfloat162 m24 = __hmul2(s, __float2bfloat162_rn(-24.f));
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                o[e] = kv4_bf16x2(c.x, e, s, n);
-                o[4 + e] = kv4_bf16x2(c.y, e, s, n);
+                o[e] = kv4_bf16x2(c.x, e, s, m24);
+                o[4 + e] = kv4_bf16x2(c.y, e, s, m24);
               }
             } else {
-              const __half2 s = kv4_half2((byte << 7) * 0x00010001u);
-              const __half2 n = __hmul2(s, __float2half2_rn(-24.f));
+              const __half2 s = kv4_half2((y << 7) * 0x00010001u);
+              const __half2 m24 = __hmul2(s, __float2half2_rn(-24.f));
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                o[e] = kv4_f16x2(c.x, e, s, n);
-                o[4 + e] = kv4_f16x2(c.y, e, s, n);
+                o[e] = kv4_f16x2(c.x, e, s, m24);
+                o[4 + e] = kv4_f16x2(c.y, e, s, m24);
               }
             }
-            uint8_t* r = dst + a * G::kAtom + key * 128;
-            *reinterpret_cast<uint4*>(r + (((2 * grp) ^ (key & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(r + (((2 * grp + 1) ^ (key & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4*>(dst + i * 1024) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst2 + i * 1024) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[st]);
+        if (lane == 0) mbar_arrive(&(kv ? v_full : k_full)[st]);
       }
-      __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(&raw_empty[rs]);
     }
     if (!ok) flags[0] = 1;
-  } else if (warp >= 4) {
+  } else {
     const int t = (warp - 4) >> 2;
     if (t < nt)
-      kv4_softmax_tile<HD>(p, rq, tmem_base, s_full, p_full, o_final, flags, t, R0, g, sp, ks, ke, nblk);
+      kv4_softmax_tile<HD>(p, rq, tmem_base, s_full, s_read, p_full, pv_done, flags, t, nt, R0, g, sp, ks, ke, nblk);
   }
   __syncwarp();
   tc_fence_before();
