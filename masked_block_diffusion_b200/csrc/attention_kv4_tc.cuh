@@ -7,7 +7,7 @@
 // tiles read the same unpacked K and V; the two tiles' softmaxes alternate with each other's
 // products on the tensor pipe.
 //
-// Roles (512 threads):
+// Roles (640 threads, five warpgroups):
 //   warps 0, 1   each issues one tile's products (warp 0 holds the TMEM allocation): S_t = Q_t K^T
 //                (bf16) into tile t's S columns, and O_t += P_t V (fp16) with P_t read from
 //                TMEM. A wait and an issue cost such a warp some 200 cycles each among the busy
@@ -20,12 +20,14 @@
 //   warps 4..7   softmax of tile 0, warps 8..11 of tile 1: one row per thread (TMEM lane), 64
 //                scores in registers, lazy reference as in attention_kv4.cuh; O is rescaled in
 //                TMEM when the reference moves (rare), and read and written out at the end;
-//   the others   (2, 3, 12..15) unpack: K to bf16 and V to fp16, both exact, as 64-dim atoms of
-//                128-byte rows with the 128-byte swizzle (K's rows are keys, K-major; V's are the
-//                same rows read as the MN-major operand). Eight consecutive lanes write 4 groups
-//                of 2 adjacent keys: 8 different 16-byte columns, no bank conflict. The packed
-//                bytes come straight into registers, a block of keys ahead, and the page ids two
-//                blocks ahead.
+//   warps 12..19 unpack 8 keys of each block of 64, K to bf16 and V to fp16, both exact, as 64-dim
+//                atoms of 128-byte rows with the 128-byte swizzle (K's rows are keys, K-major; V's
+//                are the same rows read as the MN-major operand). Eight consecutive lanes write
+//                4 groups of 2 adjacent keys: 8 different 16-byte columns, no bank conflict. The
+//                packed bytes come straight into registers, a block of keys ahead, and the page
+//                id two blocks ahead.
+// Registers: the launch gives every thread 96; the softmax warpgroups take 136 and leave 72 to the
+// unpacking ones and 64 to the first (2 x 136 + 2 x 72 + 64 = 5 x 96).
 // TMEM: S_t at 64 t, then P, then O_t. At head_dim 176 there is room for one P (32 columns) beside
 // 2 x 64 columns of S and 2 x 176 of O: the tiles use it in turn, each writing once the other's
 // product has read it. Smaller heads have a P for each tile.
@@ -72,15 +74,20 @@ struct AttnKv4TcCfg {
   static constexpr int kPCol = 2 * BK;
   static constexpr int kOCol = kPCol + (kOneP ? 1 : 2) * (BK / 2);
   static constexpr int kTmemCols = 512;
-  static constexpr int THREADS = 512;
-  // An unpacking warp has OCT groups of 8 keys of one atom of K and of V; UNPACK warps cover a block.
-  static constexpr int OCT = ATOMS == 1 ? 2 : 4;
-  static constexpr int UNPACK = ATOMS * 8 / OCT;
-  static_assert(UNPACK <= 6, "warps 2, 3, 12..15");
+  static constexpr int UNPACK = BK / 8;                  // unpacking warps
+  static constexpr int THREADS = 32 * (4 + 8 + UNPACK);
+  static constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsUnpack = 72, kRegsIssue = 64;
+  static_assert(THREADS == 640 && 2 * kRegsSoftmax + 2 * kRegsUnpack + kRegsIssue <= 5 * kRegsLaunch, "register shares");
   static_assert(kOCol + 2 * HD <= kTmemCols, "TMEM");
   static_assert(kTotal <= 232448, "shared memory");
   static_assert(kOffBar % 16 == 0, "barriers");
 };
+
+// Gives registers back or takes some of those given back, for the executing warpgroup.
+template <int N>
+DLLM_DEV void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+DLLM_DEV void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // Two fp32 operations in one instruction.
 DLLM_DEV uint64_t pack_f32x2(float a, float b) {
@@ -310,7 +317,8 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
   pdl_trigger();   // after the TMEM allocation
   const uint32_t tmem_base = *tmem_slot;
 
-  if (warp < 2) {
+  if (warp < 4) {
+    regs_dec<G::kRegsIssue>();
     if (warp < nt) {
       // ---------------- MMA issuer of tile `warp`: the warp waits as one, an elected lane issues
       const int t = __shfl_sync(0xffffffffu, warp, 0);
@@ -361,18 +369,15 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
       mbar_drain(&drain[t], 0);
       __syncwarp();
     }
-  } else if (warp < 4 || warp >= 12) {
-    // ---------------- unpacking
-    const int u = warp < 4 ? warp - 2 : warp >= 14 ? warp - 12 : warp - 8;   // 2, 3, 14, 15, 12, 13
-    constexpr int OCT = G::OCT;
-    const int a = u / (8 / OCT);                                 // the warp's atom
-    const int grp = lane & 3, gg = 4 * a + grp;
-    const int key0 = 8 * OCT * (u % (8 / OCT)) + (lane >> 2);    // the thread's keys of a block: key0 + 8 i, i < OCT
+  } else if (warp >= 12) {
+    regs_dec<G::kRegsUnpack>();
+    // ---------------- unpacking: the warp's 8 keys of each block, lane / 4 the key, lane % 4 the group of an atom
+    const int k8 = lane >> 2, grp = lane & 3;
+    const int key = 8 * (warp - 12) + k8;
     const int* trow = p.table + (long)b * p.stride;
     const int mask = (1 << p.c.page_shift) - 1;
-    const bool mine = u < G::UNPACK;
-    // page id of key `key` of block j; -1 past the end, and for an id that is no page
-    auto page_of = [&](int j, int key) -> int {
+    // page id of the key in block j; -1 past the end, and for an id that is no page
+    auto page_of = [&](int j) -> int {
       const int t = ks + j * BK + key;
       if (j >= nblk || t >= ke) return -1;
       const int id = trow[t >> p.c.page_shift];
@@ -383,54 +388,44 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     const long v_rows = (long)p.c.Hkv << p.c.page_shift, page_rows = 2 * v_rows;
     const long v_code = v_rows * (HD / 2), v_scale = v_rows * (HD / 16);
     const int head_row = g << p.c.page_shift;
-    uint2 code[2][OCT];
-    uint32_t byte[2][OCT];
-    int id[OCT / 2];   // keys 16 m .. 16 m + 15 are in one page
-    // the next block's bytes: keys that do not exist get scale 0, so become 0
-    auto fetch = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < OCT; ++i) {
-        const bool have = id[i / 2] >= 0 && ks + j * BK + key0 + 8 * i < ke && 16 * gg < HD;
-        const long r = max(id[i / 2], 0) * page_rows + (head_row + ((ks + j * BK + key0 + 8 * i) & mask));
-        const uint8_t* pc = p.c.codes + r * (HD / 2) + 8 * gg;
-        const uint8_t* ps = p.c.scales + r * (HD / 16) + gg;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          code[kv][i] = make_uint2(0, 0);
-          byte[kv][i] = 0;
-          if (have) {
-            code[kv][i] = *reinterpret_cast<const uint2*>(pc + (kv ? v_code : 0));
-            byte[kv][i] = ps[kv ? v_scale : 0];
-          }
-        }
-      }
-    };
-    auto pages = [&](int j) {
-#pragma unroll
-      for (int m = 0; m < OCT / 2; ++m) id[m] = page_of(j, key0 - (lane >> 2) + 16 * m);
-    };
-    const uint32_t at0 = a * G::kAtom + key0 * 128 + (((2 * grp) ^ (key0 & 7)) << 4);
-    bool ok = true;
-    if (mine) {
-      pages(0);
-      fetch(0);
-      pages(1);
-    }
-    for (int j = 0; j < nblk && ok && mine; ++j) {
-      // this block's bytes have had a block's time to arrive; all loads of the next one are issued
-      // together before any is waited for again
-      uint2 now[2][OCT];
-      uint32_t scale[2][OCT];
+    uint2 code[2][AT];
+    uint32_t byte[2][AT];
+    // a block's bytes; a key that does not exist has scale 0 and becomes 0
+    auto fetch = [&](int j, int id) {
+      const long r = max(id, 0) * page_rows + (head_row + ((ks + j * BK + key) & mask));
+      const uint8_t* pc = p.c.codes + r * (HD / 2) + 8 * grp;
+      const uint8_t* ps = p.c.scales + r * (HD / 16) + grp;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
-        for (int i = 0; i < OCT; ++i) {
-          now[kv][i] = code[kv][i];
-          scale[kv][i] = byte[kv][i];
-          asm volatile("" : "+r"(now[kv][i].x), "+r"(now[kv][i].y), "+r"(scale[kv][i]));
+        for (int a = 0; a < AT; ++a) {
+          code[kv][a] = make_uint2(0, 0);
+          byte[kv][a] = 0;
+          if (id >= 0 && 16 * (4 * a + grp) < HD) {
+            code[kv][a] = *reinterpret_cast<const uint2*>(pc + (kv ? v_code : 0) + 32 * a);
+            byte[kv][a] = ps[(kv ? v_scale : 0) + 4 * a];
+          }
         }
-      fetch(j + 1);
-      pages(j + 2);
+    };
+    const uint32_t at0 = key * 128 + (((2 * grp) ^ k8) << 4);
+    fetch(0, page_of(0));
+    int id = page_of(1);
+    bool ok = true;
+    for (int j = 0; j < nblk && ok; ++j) {
+      // this block's bytes have had a block's time to arrive; all loads of the next one are issued
+      // together before any is waited for again
+      uint2 now[2][AT];
+      uint32_t scale[2][AT];
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int a = 0; a < AT; ++a) {
+          now[kv][a] = code[kv][a];
+          scale[kv][a] = byte[kv][a];
+          asm volatile("" : "+r"(now[kv][a].x), "+r"(now[kv][a].y), "+r"(scale[kv][a]));
+        }
+      fetch(j + 1, id);
+      id = page_of(j + 2);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const int n = kv ? VST : KST, st = j % n;
@@ -440,14 +435,13 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
         }
         uint8_t* dst = (kv ? sV : sK) + st * G::kKV + at0;
         uint8_t* dst2 = (kv ? sV : sK) + st * G::kKV + (at0 ^ 16);
-        if (16 * gg < HD) {
 #pragma unroll
-          for (int i = 0; i < OCT; ++i) {
-            const uint2 c = now[kv][i];
-            const uint32_t y = scale[kv][i];
+        for (int a = 0; a < AT; ++a) {
+          if (16 * (4 * a + grp) < HD) {
+            const uint2 c = now[kv][a];
             uint32_t o[8];
             if (kv == 0) {
-              const __nv_bfloat162 s = kv4_scale_bf16x2(y);
+              const __nv_bfloat162 s = kv4_scale_bf16x2(scale[kv][a]);
               const __nv_bfloat162 m24 = __hmul2(s, __float2bfloat162_rn(-24.f));
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -455,7 +449,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
                 o[4 + e] = kv4_bf16x2(c.y, e, s, m24);
               }
             } else {
-              const __half2 s = kv4_half2((y << 7) * 0x00010001u);
+              const __half2 s = kv4_half2((scale[kv][a] << 7) * 0x00010001u);
               const __half2 m24 = __hmul2(s, __float2half2_rn(-24.f));
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -463,8 +457,8 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
                 o[4 + e] = kv4_f16x2(c.y, e, s, m24);
               }
             }
-            *reinterpret_cast<uint4*>(dst + i * 1024) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst2 + i * 1024) = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4*>(dst + a * G::kAtom) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst2 + a * G::kAtom) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
         fence_proxy_async_smem();
@@ -474,6 +468,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     }
     if (!ok) flags[0] = 1;
   } else {
+    regs_inc<G::kRegsSoftmax>();
     const int t = (warp - 4) >> 2;
     if (t < nt)
       kv4_softmax_tile<HD>(p, rq, tmem_base, s_full, s_read, p_full, pv_done, flags, t, nt, R0, g, sp, ks, ke, nblk);
