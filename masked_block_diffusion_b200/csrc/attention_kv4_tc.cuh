@@ -386,33 +386,31 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
       return -1;
     };
     const long v_rows = (long)p.c.Hkv << p.c.page_shift, page_rows = 2 * v_rows;
-    const long v_code = v_rows * (HD / 2), v_scale = v_rows * (HD / 16);
     const int head_row = g << p.c.page_shift;
     uint2 code[2][AT];
     uint32_t byte[2][AT];
-    // a block's bytes; a key that does not exist has scale 0 and becomes 0
-    auto fetch = [&](int j, int id) {
-      const long r = max(id, 0) * page_rows + (head_row + ((ks + j * BK + key) & mask));
+    // a block's bytes of K or V; a key that does not exist has scale 0 and becomes 0
+    auto fetch = [&](int kv, int j, int id) {
+      const long r = max(id, 0) * page_rows + (head_row + ((ks + j * BK + key) & mask)) + (kv ? v_rows : 0);
       const uint8_t* pc = p.c.codes + r * (HD / 2) + 8 * grp;
       const uint8_t* ps = p.c.scales + r * (HD / 16) + grp;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-        for (int a = 0; a < AT; ++a) {
-          code[kv][a] = make_uint2(0, 0);
-          byte[kv][a] = 0;
-          if (id >= 0 && 16 * (4 * a + grp) < HD) {
-            code[kv][a] = *reinterpret_cast<const uint2*>(pc + (kv ? v_code : 0) + 32 * a);
-            byte[kv][a] = ps[(kv ? v_scale : 0) + 4 * a];
-          }
+      for (int a = 0; a < AT; ++a) {
+        code[kv][a] = make_uint2(0, 0);
+        byte[kv][a] = 0;
+        if (id >= 0 && 16 * (4 * a + grp) < HD) {
+          code[kv][a] = *reinterpret_cast<const uint2*>(pc + 32 * a);
+          byte[kv][a] = ps[4 * a];
         }
+      }
     };
     const uint32_t at0 = key * 128 + (((2 * grp) ^ k8) << 4);
-    fetch(0, page_of(0));
-    int id = page_of(1);
+    // K runs a block ahead of V, as S runs ahead of P V: the turns are K(0), K(1), V(0), K(2), V(1), ...
+    int id_v = page_of(0), id_k = page_of(1);
+    fetch(0, 0, id_v);
     bool ok = true;
-    for (int j = 0; j < nblk && ok; ++j) {
-      // this block's bytes have had a block's time to arrive; all loads of the next one are issued
+    for (int j = -1; j < nblk && ok; ++j) {
+      // this turn's bytes have had a block's time to arrive; all loads of the next one are issued
       // together before any is waited for again
       uint2 now[2][AT];
       uint32_t scale[2][AT];
@@ -420,16 +418,21 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
       for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
         for (int a = 0; a < AT; ++a) {
+          if (kv == 1 && j < 0) continue;
           now[kv][a] = code[kv][a];
           scale[kv][a] = byte[kv][a];
           asm volatile("" : "+r"(now[kv][a].x), "+r"(now[kv][a].y), "+r"(scale[kv][a]));
         }
-      fetch(j + 1, id);
-      id = page_of(j + 2);
+      fetch(0, j + 2, id_k);
+      fetch(1, j + 1, id_v);
+      id_v = id_k;
+      id_k = page_of(j + 3);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const int n = kv ? VST : KST, st = j % n;
-        if (!__all_sync(0xffffffffu, mbar_wait(&(kv ? v_empty : k_empty)[st], ((j / n) & 1) ^ 1, flags))) {
+        const int jb = kv ? j : j + 1;
+        if (jb < 0 || jb >= nblk) continue;
+        const int n = kv ? VST : KST, st = jb % n;
+        if (!__all_sync(0xffffffffu, mbar_wait(&(kv ? v_empty : k_empty)[st], ((jb / n) & 1) ^ 1, flags))) {
           ok = false;
           break;
         }
