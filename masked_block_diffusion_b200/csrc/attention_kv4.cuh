@@ -437,62 +437,71 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
   }
 }
 
-// Joins the splits of one query: one warp per head. Grid (max_q, B).
+// Joins the splits of one query and head per block: grid (max_q * H, B). Every split of every row
+// has written its partial (0 with lse = -inf where it saw no key), so the loads depend on nothing:
+// warp w takes splits w, w + 4, ... with all lanes' loads in flight, and the warps' sums are added in
+// shared memory. (One warp per head that looked at each split's lse first took 20 us for 34 splits.)
 template <int HD>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(128)
 attn_kv4_merge_kernel(const __grid_constant__ AttnKv4Params p) {
+  constexpr int VI = (HD + 63) / 64;
+  __shared__ float sh[4][HD + 2];
   pdl_begin();
+  const int i = blockIdx.x / p.H, h = blockIdx.x - i * p.H;
   const Kv4Req rq = kv4_request(p, blockIdx.y);
-  if (rq.skip || rq.bad || (int)blockIdx.x >= rq.n) return;
-  const long t = rq.q0 + blockIdx.x;
-  const int lane = threadIdx.x & 31;
-  // splits past every key the request's rows see wrote no partial of this row's tile: all wrote their lse
-  for (int h = threadIdx.x >> 5; h < p.H; h += blockDim.x >> 5) {
-    float mx = -INFINITY;
-    bool nan = false;
-    for (int s = lane; s < p.n_splits; s += 32) {
-      const float v = p.part_lse[((long)s * p.T + t) * p.H + h];
-      nan |= v != v;
-      mx = fmaxf(mx, v);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    nan = __any_sync(0xffffffffu, nan);
-    float acc[(HD + 63) / 64][2];
-#pragma unroll
-    for (int i = 0; i < (HD + 63) / 64; ++i) acc[i][0] = acc[i][1] = 0.f;
-    float sum = 0.f;
-    if (mx != -INFINITY) {
-      for (int s = 0; s < p.n_splits; ++s) {
-        const long at = ((long)s * p.T + t) * p.H + h;
-        const float w = exp2f(p.part_lse[at] - mx);
-        if (w == 0.f) continue;
-        sum += w;
-        const float* po = p.part_o + at * HD;
-#pragma unroll
-        for (int i = 0; i < (HD + 63) / 64; ++i) {
-          const int d = 64 * i + 2 * lane;
-          if (d < HD) {
-            const float2 v = *reinterpret_cast<const float2*>(po + d);
-            acc[i][0] += w * v.x;
-            acc[i][1] += w * v.y;
-          }
-        }
-      }
-    }
-    const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
-    const float qnan = __int_as_float(0x7FC00000);
-#pragma unroll
-    for (int i = 0; i < (HD + 63) / 64; ++i) {
-      const int d = 64 * i + 2 * lane;
-      if (d < HD)
-        *reinterpret_cast<uint32_t*>(p.out + t * p.o_tok + h * p.o_head + d) =
-            (uint32_t)f32_to_bf16_any(nan ? qnan : acc[i][0] * inv) |
-            ((uint32_t)f32_to_bf16_any(nan ? qnan : acc[i][1] * inv) << 16);
-    }
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[t * p.H + h] = nan ? qnan : mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+  if (rq.skip || rq.bad || i >= rq.n) return;
+  const long t = rq.q0 + i;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float* lse = p.part_lse + t * p.H + h;
+  const float* po = p.part_o + (t * p.H + h) * HD + 2 * lane;
+  const long row = (long)p.T * p.H;
+  float mx = -INFINITY;
+  bool nan = false;
+  for (int s = lane; s < p.n_splits; s += 32) {
+    const float v = lse[s * row];
+    nan |= v != v;
+    mx = fmaxf(mx, v);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  nan = __any_sync(0xffffffffu, nan);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  float acc[VI][2], sum = 0.f;
+#pragma unroll
+  for (int v = 0; v < VI; ++v) acc[v][0] = acc[v][1] = 0.f;
+#pragma unroll 4
+  for (int s = warp; s < p.n_splits; s += 4) {
+    const float w = exp2f(lse[s * row] - ref);
+    float2 x[VI];
+#pragma unroll
+    for (int v = 0; v < VI; ++v)
+      x[v] = 64 * v + 2 * lane < HD ? *reinterpret_cast<const float2*>(po + s * row * HD + 64 * v) : make_float2(0.f, 0.f);
+    sum += w;
+#pragma unroll
+    for (int v = 0; v < VI; ++v) {
+      acc[v][0] += w * x[v].x;
+      acc[v][1] += w * x[v].y;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < VI; ++v)
+    if (64 * v + 2 * lane < HD) {
+      sh[warp][64 * v + 2 * lane] = acc[v][0];
+      sh[warp][64 * v + 2 * lane + 1] = acc[v][1];
+    }
+  if (lane == 0) sh[warp][HD] = sum;
+  __syncthreads();
+  const float all = sh[0][HD] + sh[1][HD] + sh[2][HD] + sh[3][HD];
+  const float inv = mx == -INFINITY ? 0.f : 1.f / all;
+  const float qnan = __int_as_float(0x7FC00000);
+  for (int d = 2 * threadIdx.x; d < HD; d += 256) {
+    const float a = (sh[0][d] + sh[1][d] + sh[2][d] + sh[3][d]) * inv;
+    const float b = (sh[0][d + 1] + sh[1][d + 1] + sh[2][d + 1] + sh[3][d + 1]) * inv;
+    *reinterpret_cast<uint32_t*>(p.out + t * p.o_tok + h * p.o_head + d) =
+        (uint32_t)f32_to_bf16_any(nan ? qnan : a) | ((uint32_t)f32_to_bf16_any(nan ? qnan : b) << 16);
+  }
+  if (threadIdx.x == 0 && p.lse != nullptr)
+    p.lse[t * p.H + h] = nan ? qnan : mx == -INFINITY ? -INFINITY : (mx + log2f(all)) * 0.6931471805599453f;
 }
 
 }  // namespace dllm

@@ -118,11 +118,20 @@ AttnPlan attn_plan(int B, int max_q, int max_kv, int group, int Hkv) {
   const long rows = (long)max_q * group;
   a.nr = rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
   a.tiles = ceil_div(rows, a.nr ? 8 * a.nr : 256);
-  // Keys are split until the blocks fill the SMs' slots, but no split has fewer than 128 keys.
+  // Blocks that the GPU holds at a time, and blocks without a split.
   const long slots = kSMs * (a.nr == 1 ? 3 : a.nr == 2 ? 2 : 1);
   const long blocks = (long)B * Hkv * a.tiles;
-  const long fill = a.nr ? (slots + blocks - 1) / blocks : slots / blocks;
-  const long want = std::max(1L, std::min(fill, (max_kv + 127L) / 128));
+  long want;
+  if (a.nr == 0) {
+    want = slots / blocks;
+  } else if (blocks * ceil_div(max_kv, 256) <= slots) {
+    want = ceil_div(max_kv, 64);                       // a short call: as wide as it goes
+  } else {
+    // one wave of blocks when a few requests share the GPU; else blocks of 512 keys or more and
+    // about four waves of them, so that requests of different lengths even out
+    want = blocks >= slots / 4 ? std::min<long>(ceil_div(4 * slots, blocks), ceil_div(max_kv, 512)) : slots / blocks;
+  }
+  want = std::max(1L, std::min<long>(want, ceil_div(max_kv, a.nr ? 64 : 128)));
   a.chunk = std::max(64, ceil_div(ceil_div(max_kv, want), 64) * 64);
   a.n_splits = std::max(1, ceil_div(max_kv, a.chunk));
   return a;
@@ -163,7 +172,7 @@ template <int HD>
 cudaError_t run_attn(cudaStream_t st, const AttnPlan& a, const AttnKv4Params& p) {
   cudaError_t e = a.nr == 1 ? run_few<HD, 1>(st, a, p) : a.nr == 2 ? run_few<HD, 2>(st, a, p) : run_tc<HD>(st, a, p);
   if (e == cudaSuccess && a.n_splits > 1)
-    e = launch(st, attn_kv4_merge_kernel<HD>, dim3(p.max_q, p.B), 256, 0, p);
+    e = launch(st, attn_kv4_merge_kernel<HD>, dim3((unsigned)p.max_q * p.H, p.B), 128, 0, p);
   return e;
 }
 
