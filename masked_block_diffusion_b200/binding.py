@@ -309,37 +309,47 @@ def dllm_rope_init(rotary_dim, layout, theta, scaling, factor, original_ctx, bet
     return r
 
 
+# The operations below may run many times a step: the library is looked up once, errors on the way out.
+
 def dllm_op_rope(rope: dllm_rope, x_ptr, x_type, x_token_stride, x_head_stride, pos_ptr, T, H, head_dim, y_ptr, y_type,
                  y_token_stride, y_head_stride, transposed, stream_ptr):
-    _check(load().dllm_op_rope(rope, x_ptr, x_type, x_token_stride, x_head_stride, pos_ptr, T, H, head_dim, y_ptr,
-                               y_type, y_token_stride, y_head_stride, transposed, stream_ptr), "dllm_op_rope")
+    code = (_lib or load()).dllm_op_rope(rope, x_ptr, x_type, x_token_stride, x_head_stride, pos_ptr, T, H, head_dim,
+                                         y_ptr, y_type, y_token_stride, y_head_stride, transposed, stream_ptr)
+    if code:
+        _check(code, "dllm_op_rope")
 
 
 def dllm_op_append_kv4(cache: dllm_kv4, k_ptr, k_token_stride, k_head_stride, v_ptr, v_token_stride, v_head_stride, type_,
                        req_ptr, pos_ptr, rope_pos_ptr, T, table_ptr, n_req, table_stride, rope, stream_ptr):
     """rope: a dllm_rope or None; rope_pos_ptr 0: pos."""
-    _check(load().dllm_op_append_kv4(cache, k_ptr, k_token_stride, k_head_stride, v_ptr, v_token_stride, v_head_stride,
-                                     type_, req_ptr, pos_ptr, rope_pos_ptr, T, table_ptr, n_req, table_stride, rope,
-                                     stream_ptr), "dllm_op_append_kv4")
+    code = (_lib or load()).dllm_op_append_kv4(cache, k_ptr, k_token_stride, k_head_stride, v_ptr, v_token_stride,
+                                               v_head_stride, type_, req_ptr, pos_ptr, rope_pos_ptr, T, table_ptr,
+                                               n_req, table_stride, rope, stream_ptr)
+    if code:
+        _check(code, "dllm_op_append_kv4")
 
 
 def dllm_op_read_kv4(cache: dllm_kv4, req_ptr, pos_ptr, T, table_ptr, n_req, table_stride, k_out_ptr, v_out_ptr,
                      stream_ptr):
-    _check(load().dllm_op_read_kv4(cache, req_ptr, pos_ptr, T, table_ptr, n_req, table_stride, k_out_ptr, v_out_ptr,
-                                   stream_ptr), "dllm_op_read_kv4")
+    code = (_lib or load()).dllm_op_read_kv4(cache, req_ptr, pos_ptr, T, table_ptr, n_req, table_stride, k_out_ptr,
+                                             v_out_ptr, stream_ptr)
+    if code:
+        _check(code, "dllm_op_read_kv4")
 
 
 def dllm_op_attn_kv4(cache: dllm_kv4, q_ptr, q_token_stride, q_head_stride, out_ptr, out_token_stride, out_head_stride,
                      lse_ptr, q_start_ptr, kv_len_ptr, B, T, max_q, max_kv, H, table_ptr, table_stride, causal, scale,
                      workspace_ptr, workspace_bytes, stream_ptr):
-    _check(load().dllm_op_attn_kv4(cache, q_ptr, q_token_stride, q_head_stride, out_ptr, out_token_stride,
-                                   out_head_stride, lse_ptr, q_start_ptr, kv_len_ptr, B, T, max_q, max_kv, H, table_ptr,
-                                   table_stride, causal, scale, workspace_ptr, workspace_bytes, stream_ptr),
-           "dllm_op_attn_kv4")
+    code = (_lib or load()).dllm_op_attn_kv4(cache, q_ptr, q_token_stride, q_head_stride, out_ptr, out_token_stride,
+                                             out_head_stride, lse_ptr, q_start_ptr, kv_len_ptr, B, T, max_q, max_kv,
+                                             H, table_ptr, table_stride, causal, scale, workspace_ptr,
+                                             workspace_bytes, stream_ptr)
+    if code:
+        _check(code, "dllm_op_attn_kv4")
 
 
 def dllm_op_attn_kv4_workspace(cache: dllm_kv4, B, T, max_q, max_kv, H) -> int:
-    n = load().dllm_op_attn_kv4_workspace(cache, B, T, max_q, max_kv, H)
+    n = (_lib or load()).dllm_op_attn_kv4_workspace(cache, B, T, max_q, max_kv, H)
     if n < 0:
         _check(n, "dllm_op_attn_kv4_workspace")
     return n

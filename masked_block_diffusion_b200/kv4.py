@@ -13,7 +13,6 @@ streams' work on them.
 
 from __future__ import annotations
 
-import math
 from typing import Optional, Tuple
 
 import torch
@@ -45,43 +44,52 @@ class Rope:
         self.rotary_dim, self.layout, self.magnitude = int(rotary_dim), layout, self.c.magnitude
 
 
+try:   # the current device and its current stream as integers, without the objects around them
+    from torch._C import _cuda_getCurrentRawStream as _stream_of
+    from torch._C import _cuda_getDevice as _current_device
+except ImportError:   # pragma: no cover
+    _current_device = torch.cuda.current_device
+
+    def _stream_of(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 def _bad(name: str, why: str):
     raise ValueError(f"{name}: {why}")
 
 
-def _heads(name: str, t: torch.Tensor, device, shape, dtypes) -> None:
-    """A [T][heads][dim] tensor whose last dimension is contiguous."""
-    if t.device != device:
-        _bad(name, f"on {t.device}, expected {device}")
-    if t.dtype not in dtypes:
-        _bad(name, f"{t.dtype}, expected one of {[str(d) for d in dtypes]}")
-    if t.dim() != 3 or tuple(t.shape) != tuple(shape):
-        _bad(name, f"shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(2) != 1 and t.shape[2] > 1:
+# The checks below run on every call, so each takes what it looks at from the tensor once.
+
+def _heads(name: str, t: torch.Tensor, dev: int, T: int, H: int, d: int, types) -> tuple:
+    """A [T][H][d] tensor on device `dev` whose last dimension is contiguous: its (token stride, head stride), 0
+    where a dimension has one element and no stride that matters."""
+    if t.get_device() != dev:
+        _bad(name, f"on {t.device}, expected cuda:{dev}")
+    if t.dtype not in types:
+        _bad(name, f"{t.dtype}, expected one of {[str(x) for x in types]}")
+    if t.shape != (T, H, d):
+        _bad(name, f"shape {tuple(t.shape)}, expected {(T, H, d)}")
+    st, sh, sd = t.stride()
+    if sd != 1 and d > 1:
         _bad(name, "the last dimension has to be contiguous")
+    return st if T > 1 else 0, sh if H > 1 else 0
 
 
-def _ints(name: str, t: torch.Tensor, device, n: int) -> None:
-    if t.device != device:
-        _bad(name, f"on {t.device}, expected {device}")
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        _bad(name, f"expected a contiguous int32 tensor of {n}, got {t.dtype} {tuple(t.shape)}")
+def _ints(name: str, t: torch.Tensor, dev: int, n: int) -> int:
+    if t.dtype is not torch.int32 or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        _bad(name, f"expected a contiguous int32 tensor of {n} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _table(t: torch.Tensor, device) -> None:
-    if t.device != device:
-        _bad("table", f"on {t.device}, expected {device}")
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1):
-        _bad("table", f"expected int32 [requests][pages] with contiguous rows, got {t.dtype} {tuple(t.shape)}")
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _strides(t: torch.Tensor) -> Tuple[int, int]:
-    """Token and head strides; a dimension of one element has none that matters."""
-    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+def _table(t: torch.Tensor, dev: int) -> tuple:
+    """(address, rows, row stride)"""
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.get_device() != dev:
+        _bad("table", f"expected int32 [requests][pages] on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    rows, cols = t.shape
+    sr, sc = t.stride()
+    if rows < 1 or cols < 1 or (cols > 1 and sc != 1):
+        _bad("table", f"expected at least one row and page, and contiguous rows: {tuple(t.shape)}")
+    return t.data_ptr(), rows, sr if rows > 1 else cols
 
 
 def _no_grad(*tensors) -> None:
@@ -90,24 +98,20 @@ def _no_grad(*tensors) -> None:
                            "(rope(..., transposed=True) is the gradient of rope)")
 
 
-class _on:
-    """Makes `device` current for a launch and gives its current stream."""
+def _launch(dev: int, op, *args) -> None:
+    """op(*args, stream) with device `dev` current, on its current stream."""
+    if _current_device() == dev:
+        op(*args, _stream_of(dev))
+    else:
+        with torch.cuda.device(dev):
+            op(*args, _stream_of(dev))
 
-    def __init__(self, device: torch.device):
-        if device.type != "cuda":
-            raise ValueError(f"tensors on {device}: a CUDA device is needed")
-        self.index = device.index
-        self.guard = None
 
-    def __enter__(self) -> int:
-        if torch.cuda.current_device() != self.index:
-            self.guard = torch.cuda.device(self.index)
-            self.guard.__enter__()
-        return torch.cuda.current_stream(self.index).cuda_stream
-
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+def _device_of(name: str, t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        _bad(name, f"on {t.device}: a CUDA device is needed")
+    return dev
 
 
 def rope(x: torch.Tensor, pos: torch.Tensor, plan: Rope, out: Optional[torch.Tensor] = None,
@@ -118,23 +122,21 @@ def rope(x: torch.Tensor, pos: torch.Tensor, plan: Rope, out: Optional[torch.Ten
     of out_dtype (x's type by default). transposed: the transposed map, i.e. the gradient."""
     if x.dim() != 3:
         _bad("x", f"expected [T][heads][head_dim], got {tuple(x.shape)}")
-    _heads("x", x, x.device, x.shape, _TYPES)
-    _no_grad(x, out)
+    dev = _device_of("x", x)
     T, H, hd = x.shape
-    _ints("pos", pos, x.device, T)
+    xt, xh = _heads("x", x, dev, T, H, hd, _TYPES)
+    _no_grad(x, out)
+    at = _ints("pos", pos, dev, T)
     if out is None:
         dtype = out_dtype or x.dtype
         if dtype not in _TYPES:
             _bad("out_dtype", f"{dtype}, expected one of {[str(d) for d in _TYPES]}")
-        out = torch.empty((T, H, hd), dtype=dtype, device=x.device)
-    else:
-        _heads("out", out, x.device, x.shape, _TYPES)
-        if out_dtype is not None and out_dtype != out.dtype:
-            _bad("out", f"{out.dtype}, but out_dtype is {out_dtype}")
-    with _on(x.device) as stream:
-        binding.dllm_op_rope(plan.c, x.data_ptr(), _TYPES[x.dtype], *_strides(x), pos.data_ptr(), T, H, hd,
-                             out.data_ptr(), _TYPES[out.dtype], *_strides(out), 1 if transposed else 0,
-                             stream)
+        out = x.new_empty((T, H, hd), dtype=dtype)
+    elif out_dtype is not None and out_dtype != out.dtype:
+        _bad("out", f"{out.dtype}, but out_dtype is {out_dtype}")
+    yt, yh = _heads("out", out, dev, T, H, hd, _TYPES)
+    _launch(dev, binding.dllm_op_rope, plan.c, x.data_ptr(), _TYPES[x.dtype], xt, xh, at, T, H, hd, out.data_ptr(),
+            _TYPES[out.dtype], yt, yh, 1 if transposed else 0)
     return out
 
 
@@ -178,8 +180,7 @@ class KVCache4:
         self.head_dim = 2 * codes.shape[4]
         self.c = binding.dllm_kv4(codes.data_ptr(), scales.data_ptr(), self.n_pages, self.page, self.n_kv_heads,
                                   self.head_dim)
-        if self.device.type != "cuda":
-            _bad("codes, scales", f"on {self.device}: a CUDA device is needed")
+        self._dev = _device_of("codes, scales", codes)
         # the library's own check of the sizes
         binding.dllm_op_attn_kv4_workspace(self.c, 0, 0, 0, 0, self.n_kv_heads)
 
@@ -187,42 +188,31 @@ class KVCache4:
                rope: Optional[Rope] = None, rope_pos: Optional[torch.Tensor] = None) -> None:
         """Writes k, v [T][n_kv_heads][head_dim] (one type, fp32 or bf16, strided) to positions pos of
         table rows req (int32 [T]; req < 0: padding), k rotated by `rope` to rope_pos (pos by default)."""
-        T = k.shape[0]
-        shape = (T, self.n_kv_heads, self.head_dim)
-        _heads("k", k, self.device, shape, _TYPES)
-        _heads("v", v, self.device, shape, (k.dtype,))
+        T, H, d, dev = k.shape[0], self.n_kv_heads, self.head_dim, self._dev
+        kt, kh = _heads("k", k, dev, T, H, d, _TYPES)
+        vt, vh = _heads("v", v, dev, T, H, d, (k.dtype,))
         _no_grad(k, v)
-        _ints("req", req, self.device, T)
-        _ints("pos", pos, self.device, T)
-        _table(table, self.device)
-        if rope_pos is not None:
-            _ints("rope_pos", rope_pos, self.device, T)
-        with _on(self.device) as stream:
-            binding.dllm_op_append_kv4(self.c, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), _TYPES[k.dtype], req.data_ptr(), pos.data_ptr(),
-                                       None if rope_pos is None else rope_pos.data_ptr(), T, table.data_ptr(),
-                                       table.shape[0], _row_stride(table), None if rope is None else rope.c, stream)
+        _launch(dev, binding.dllm_op_append_kv4, self.c, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _TYPES[k.dtype],
+                _ints("req", req, dev, T), _ints("pos", pos, dev, T),
+                None if rope_pos is None else _ints("rope_pos", rope_pos, dev, T), T, *_table(table, dev),
+                None if rope is None else rope.c)
 
     def read(self, req: torch.Tensor, pos: torch.Tensor, table: torch.Tensor, k_out: Optional[torch.Tensor] = None,
              v_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
         """Positions pos of table rows req as bf16 (k, v), each [T][n_kv_heads][head_dim]. Rows of padding
         (req < 0) are left as they were in k_out and v_out, and are zero in outputs made here."""
-        T = req.shape[0]
-        shape = (T, self.n_kv_heads, self.head_dim)
-        _ints("req", req, self.device, T)
-        _ints("pos", pos, self.device, T)
-        _table(table, self.device)
+        T, H, d, dev = req.shape[0], self.n_kv_heads, self.head_dim, self._dev
         outs = []
         for name, t in (("k_out", k_out), ("v_out", v_out)):
             if t is None:
-                t = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+                t = self.codes.new_zeros((T, H, d), dtype=torch.bfloat16)
             else:
-                _heads(name, t, self.device, shape, (torch.bfloat16,))
+                _heads(name, t, dev, T, H, d, (torch.bfloat16,))
                 if not t.is_contiguous():
                     _bad(name, "has to be contiguous")
             outs.append(t)
-        with _on(self.device) as stream:
-            binding.dllm_op_read_kv4(self.c, req.data_ptr(), pos.data_ptr(), T, table.data_ptr(), table.shape[0],
-                                     _row_stride(table), outs[0].data_ptr(), outs[1].data_ptr(), stream)
+        _launch(dev, binding.dllm_op_read_kv4, self.c, _ints("req", req, dev, T), _ints("pos", pos, dev, T), T,
+                *_table(table, dev), outs[0].data_ptr(), outs[1].data_ptr())
         return outs[0], outs[1]
 
     def attend(self, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor, max_q: int,
@@ -238,31 +228,28 @@ class KVCache4:
         if q.dim() != 3:
             _bad("q", f"expected [T][heads][head_dim], got {tuple(q.shape)}")
         T, H, hd = q.shape
-        _heads("q", q, self.device, (T, H, self.head_dim), (torch.bfloat16,))
+        dev, B = self._dev, kv_len.shape[0]
+        qt, qh = _heads("q", q, dev, T, H, self.head_dim, (torch.bfloat16,))
         _no_grad(q)
-        B = kv_len.shape[0]
-        _ints("kv_len", kv_len, self.device, B)
-        _ints("q_start", q_start, self.device, B + 1)
-        _table(table, self.device)
-        if table.shape[0] < B:
-            _bad("table", f"{table.shape[0]} rows for {B} requests")
+        tab, rows, stride = _table(table, dev)
+        if rows < B:
+            _bad("table", f"{rows} rows for {B} requests")
         if out is None:
-            out = torch.empty((T, H, hd), dtype=torch.bfloat16, device=self.device)
-        else:
-            _heads("out", out, self.device, (T, H, hd), (torch.bfloat16,))
-        lse = torch.empty((T, H), dtype=torch.float32, device=self.device) if return_lse else None
-        need = self.workspace_bytes(B, T, max_q, max_kv, H)
+            out = q.new_empty((T, H, hd))
+        ot, oh = _heads("out", out, dev, T, H, hd, (torch.bfloat16,))
+        lse = q.new_empty((T, H), dtype=torch.float32) if return_lse else None
         if workspace is None:
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-        elif workspace.device != self.device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-            _bad("workspace", "expected a contiguous uint8 tensor on the cache's device")
-        with _on(self.device) as stream:
-            binding.dllm_op_attn_kv4(self.c, q.data_ptr(), *_strides(q), out.data_ptr(), *_strides(out), None if lse is None else lse.data_ptr(), q_start.data_ptr(),
-                                     kv_len.data_ptr(), B, T, max_q, max_kv, H, table.data_ptr(), _row_stride(table),
-                                     1 if causal else 0, 1.0 / math.sqrt(hd) if scale is None else scale,
-                                     None if workspace is None else workspace.data_ptr(),
-                                     0 if workspace is None else workspace.numel(), stream)
+            size = self.workspace_bytes(B, T, max_q, max_kv, H)
+            if size:
+                workspace = self.codes.new_empty(size)
+        else:
+            if workspace.get_device() != dev or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+                _bad("workspace", "expected a contiguous uint8 tensor on the cache's device")
+            size = workspace.numel()
+        _launch(dev, binding.dllm_op_attn_kv4, self.c, q.data_ptr(), qt, qh, out.data_ptr(), ot, oh,
+                lse.data_ptr() if return_lse else None, _ints("q_start", q_start, dev, B + 1),
+                _ints("kv_len", kv_len, dev, B), B, T, max_q, max_kv, H, tab, stride, 1 if causal else 0,
+                hd ** -0.5 if scale is None else scale, None if workspace is None else workspace.data_ptr(), size)
         return (out, lse) if return_lse else out
 
     def workspace_bytes(self, B: int, T: int, max_q: int, max_kv: int, heads: int) -> int:
