@@ -337,7 +337,8 @@ int dllm_rope_init(dllm_rope* out, int rotary_dim, int layout, double theta, int
                    double original_ctx, double beta_fast, double beta_slow);
 
 /* y[t][h] = x[t][h] rotated to position pos[t] (device int32 [T]); dims from rotary_dim on are
- * copied. x and y are DLLM_F32 or DLLM_BF16, each with its own strides, head_dim <= 1024.
+ * copied. x and y are DLLM_F32 or DLLM_BF16, each with its own strides; head_dim <= 1024,
+ * H <= 32768, H * head_dim <= 2^20.
  * y == x with equal type and strides is allowed; other overlaps are not. transposed = 1
  * applies the transposed map, which is the gradient: with dy given as x it writes dx to y.
  * Angles are reduced in 64 bits, cos and sin rounded to fp32 once, products and sums in fp32,
@@ -377,10 +378,11 @@ int dllm_op_append_kv4(const dllm_kv4* cache, const void* k, long long k_token_s
                        int n_req, int table_stride, const dllm_rope* rope, void* stream);
 
 /* Reads positions back as bf16: k_out and v_out [T][n_kv_heads][head_dim], contiguous and 16-byte
- * aligned, either may be NULL. Token t is position pos[t] of row req[t]; req < 0: its rows of the
- * outputs are left as they were; a row, position or page that does not exist reads NaN. */
+ * aligned, either may be NULL. Token t is position pos[t] of row req[t]; req < 0 is padding: its rows
+ * of the outputs are left as they were, or with zero_padding = 1 zeroed; a row, position or page
+ * that does not exist reads NaN. */
 int dllm_op_read_kv4(const dllm_kv4* cache, const int32_t* req, const int32_t* pos, int T, const int32_t* table,
-                     int n_req, int table_stride, uint16_t* k_out, uint16_t* v_out, void* stream);
+                     int n_req, int table_stride, uint16_t* k_out, uint16_t* v_out, int zero_padding, void* stream);
 
 /* Attention of a batch's queries over the cache. Request b's queries are rows q_start[b] ..
  * q_start[b + 1] - 1 of q (bf16 [T][H][head_dim] with strides that are multiples of 8, 16-byte

@@ -142,7 +142,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                               _vp]),
         "dllm_op_append_kv4": (_i, [ctypes.POINTER(dllm_kv4), _vp, _ll, _ll, _vp, _ll, _ll, _i, _vp, _vp, _vp, _i, _vp,
                                     _i, _i, ctypes.POINTER(dllm_rope), _vp]),
-        "dllm_op_read_kv4": (_i, [ctypes.POINTER(dllm_kv4), _vp, _vp, _i, _vp, _i, _i, _vp, _vp, _vp]),
+        "dllm_op_read_kv4": (_i, [ctypes.POINTER(dllm_kv4), _vp, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _vp]),
         "dllm_op_attn_kv4": (_i, [ctypes.POINTER(dllm_kv4), _vp, _ll, _ll, _vp, _ll, _ll, _vp, _vp, _vp, _i, _i, _i, _i,
                                   _i, _vp, _i, _i, ctypes.c_float, _vp, ctypes.c_size_t, _vp]),
         "dllm_op_attn_kv4_workspace": (_ll, [ctypes.POINTER(dllm_kv4), _i, _i, _i, _i, _i]),
@@ -330,9 +330,9 @@ def dllm_op_append_kv4(cache: dllm_kv4, k_ptr, k_token_stride, k_head_stride, v_
 
 
 def dllm_op_read_kv4(cache: dllm_kv4, req_ptr, pos_ptr, T, table_ptr, n_req, table_stride, k_out_ptr, v_out_ptr,
-                     stream_ptr):
+                     zero_padding, stream_ptr):
     code = (_lib or load()).dllm_op_read_kv4(cache, req_ptr, pos_ptr, T, table_ptr, n_req, table_stride, k_out_ptr,
-                                             v_out_ptr, stream_ptr)
+                                             v_out_ptr, zero_padding, stream_ptr)
     if code:
         _check(code, "dllm_op_read_kv4")
 

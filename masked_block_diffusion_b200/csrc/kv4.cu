@@ -179,21 +179,31 @@ cudaError_t run_attn(cudaStream_t st, const AttnPlan& a, const AttnKv4Params& p)
 template <typename TI, typename TO>
 cudaError_t run_rope(cudaStream_t st, bool vec, const RopeParams& r, const void* x, long xt, long xh, const int32_t* pos,
                      int T, int H, int hd, void* y, long yt, long yh) {
-  // a block's share: about 8 K elements, so that 256 threads have a few vectors each
-  const int tb = std::max(1, std::min(16, 8192 / (H * hd)));
+  const int rot_units = vec ? (r.interleaved ? r.rd / 8 : r.rd / 16) : r.rd / 2;
+  const int head_units = rot_units + (hd - r.rd) / (vec ? 8 : 1);
+  int threads;
+  const TokenTiling tl = token_tiling(H * head_units, T, r.rd, kSMs, &threads);
   auto kern = vec ? rope_kernel<TI, TO, true> : rope_kernel<TI, TO, false>;
-  return launch(st, kern, dim3(ceil_div(T, tb)), 256, sizeof(float2) * tb * (r.rd / 2), r,
-                reinterpret_cast<const TI*>(x), xt, xh, pos, T, H, hd, reinterpret_cast<TO*>(y), yt, yh, tb);
+  return launch(st, kern, dim3(ceil_div(T, tl.tb)), threads, sizeof(float4) * tl.tb * rope_stride(r.rd), r,
+                reinterpret_cast<const TI*>(x), xt, xh, pos, T, head_units, rot_units, reinterpret_cast<TO*>(y), yt, yh,
+                tl);
+}
+
+template <int HD, typename TI>
+cudaError_t run_append_hd(cudaStream_t st, bool vec, const RopeParams& r, const Kv4& c, const Kv4Addr& a, const void* k,
+                          long kt, long kh, const void* v, long vt, long vh, const int32_t* rope_pos, int T) {
+  int threads;
+  const TokenTiling tl = token_tiling(2 * c.Hkv * (HD / 8), T, r.rd, kSMs, &threads);
+  auto kern = vec ? kv4_append_kernel<HD, TI, true> : kv4_append_kernel<HD, TI, false>;
+  return launch(st, kern, dim3(ceil_div(T, tl.tb)), threads, sizeof(float4) * tl.tb * rope_stride(r.rd), r, c, a,
+                reinterpret_cast<const TI*>(k), kt, kh, reinterpret_cast<const TI*>(v), vt, vh, rope_pos, T, tl);
 }
 
 template <typename TI>
 cudaError_t run_append(cudaStream_t st, bool vec, const RopeParams& r, const Kv4& c, const Kv4Addr& a, const void* k,
                        long kt, long kh, const void* v, long vt, long vh, const int32_t* rope_pos, int T) {
-  const int per_tok = 2 * c.Hkv * (c.hd / 16);
-  const int tb = T < 1024 ? 1 : std::max(1, std::min(8, 1024 / per_tok));
-  auto kern = vec ? kv4_append_kernel<TI, true> : kv4_append_kernel<TI, false>;
-  return launch(st, kern, dim3(ceil_div(T, tb)), 256, sizeof(float2) * tb * (r.rd / 2), r, c, a,
-                reinterpret_cast<const TI*>(k), kt, kh, reinterpret_cast<const TI*>(v), vt, vh, rope_pos, T, tb);
+  auto f = c.hd == 176 ? run_append_hd<176, TI> : c.hd == 128 ? run_append_hd<128, TI> : run_append_hd<64, TI>;
+  return f(st, vec, r, c, a, k, kt, kh, v, vt, vh, rope_pos, T);
 }
 
 }  // namespace
@@ -245,7 +255,7 @@ int dllm_op_rope(const dllm_rope* rope, const void* x, int x_type, long long x_t
                  const int32_t* pos, int T, int H, int head_dim, void* y, int y_type, long long y_token_stride,
                  long long y_head_stride, int transposed, void* stream) {
   if (!rope || (x_type != DLLM_F32 && x_type != DLLM_BF16) || (y_type != DLLM_F32 && y_type != DLLM_BF16) || T < 0 ||
-      H < 1 || H > 65536 || head_dim < 2 || head_dim > 1024 || !rope_ok(rope, head_dim))
+      H < 1 || H > 32768 || head_dim < 2 || head_dim > 1024 || (long)H * head_dim > (1 << 20) || !rope_ok(rope, head_dim))
     return DLLM_E_INVAL;
   if (T == 0) return DLLM_OK;
   if (!x || !y || !pos) return DLLM_E_INVAL;
@@ -279,16 +289,16 @@ int dllm_op_append_kv4(const dllm_kv4* cache, const void* k, long long k_token_s
 }
 
 int dllm_op_read_kv4(const dllm_kv4* cache, const int32_t* req, const int32_t* pos, int T, const int32_t* table,
-                     int n_req, int table_stride, uint16_t* k_out, uint16_t* v_out, void* stream) {
+                     int n_req, int table_stride, uint16_t* k_out, uint16_t* v_out, int zero_padding, void* stream) {
   if (!cache_ok(cache) || T < 0 || !aligned16(k_out) || !aligned16(v_out)) return DLLM_E_INVAL;
   if (T == 0 || (!k_out && !v_out)) return DLLM_OK;
   if (!addr_ok(req, pos, table, n_req, table_stride)) return DLLM_E_INVAL;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const Kv4Addr a{req, pos, table, n_req, table_stride};
-  const long units = (long)T * cache->n_kv_heads * (cache->head_dim / 16);
-  if (units > 256L * 0x7FFFFFFF) return DLLM_E_INVAL;
-  return status(launch(st, kv4_read_kernel, dim3(ceil_div(units, 256), 2), 256, 0, cache_of(cache), a, (long)T, k_out,
-                       v_out));
+  auto kern = cache->head_dim == 176   ? kv4_read_kernel<176>
+              : cache->head_dim == 128 ? kv4_read_kernel<128>
+                                       : kv4_read_kernel<64>;
+  return status(launch(st, kern, dim3(ceil_div(T, 8)), 256, 0, cache_of(cache), a, T, k_out, v_out, zero_padding));
 }
 
 long long dllm_op_attn_kv4_workspace(const dllm_kv4* cache, int B, int T, int max_q, int max_kv, int H) {

@@ -55,130 +55,174 @@ DLLM_DEV long kv4_row(const Kv4& c, int id, int kv, int head, int off) {
   return ((((long)id * 2 + kv) * c.Hkv + head) << c.page_shift) + off;
 }
 
-// The group's scale byte: the least one with 7 * scale >= top (0xD2 at most; top is not NaN).
+// The group's scale byte: the least one with 7 * scale >= top, for 0 <= top <= 7 * 2560.
+// That is top / 7 rounded up to a scale. The quotient correctly rounded to fp32 does as well as the
+// exact one: a scale s has 4 significant bits, 7 s is exact, and the next fp32 number above 7 s
+// is (at least 2^-21 / 7 = 1.14 * 2^-24 of s's binade) more than half a step of fp32 away
+// from s after the division. Rounding up is an addition to the bits below the scale's; under 2^-14 the
+// scales are 2^-17 apart, as they are just above 2^-14.
 DLLM_DEV int kv4_scale_byte(float top) {
-  if (!(top > 0.f)) return 0;
-  if (top >= 7.f * 2560.f) return kKv4MaxScale;
-  // a guess from the quotient's bits, put right by exact products (7 * scale has 7 bits)
-  int b = min((int)(__half_as_ushort(__float2half_rd(top * (1.f / 7.f))) >> 7), kKv4MaxScale);
-  if (b > 0 && 7.f * kv4_scale(b - 1) >= top) --b;
-  if (7.f * kv4_scale(b) < top) ++b;
-  return b;
+  const float seventh = 0x1.24924ap-3f;   // 1 / 7 correctly rounded; the quotient as in kv4_pack8
+  const float q0 = __fmul_rn(top, seventh);
+  const float q = __fmaf_rn(__fmaf_rn(-q0, 7.f, top), seventh, q0);
+  const bool small = q < 0x1p-14f;
+  const uint32_t bits = __float_as_uint(small ? __fadd_ru(q, 0x1p-14f) : q);
+  return (int)((bits + 0xFFFFFu) >> 20) - (small ? 904 : 896);
 }
 
-// Sixteen values to two code words and the scale byte. Nearest code, ties to even of the
-// correctly rounded quotient; beyond 7 scales saturates; NaN counts as 0.
-DLLM_DEV uint2 kv4_pack(const float (&v)[16], int& byte) {
-  float top = 0.f;
+// 1 / s of a scale, correctly rounded: the approximation improved by one Newton step (a test goes
+// through all scales).
+DLLM_DEV float kv4_reciprocal(float s) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+  return __fmaf_rn(__fmaf_rn(-s, y, 1.f), y, y);
+}
+
+DLLM_DEV float max_nan(float a, float b) {   // NaN if either is one
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Eight values, half of a group whose other half the neighbouring lane (lane ^ 1) has, to their code
+// word and the group's scale byte. The code is the correctly rounded quotient v / s to the nearest
+// integer, ties to even, + 8; beyond 7 scales saturates; NaN counts as 0.
+// The quotient: with y = 1 / s correctly rounded, q0 = v y, q = q0 + (v - q0 s) y with fused
+// operations is the correctly rounded v / s (Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990): three operations per value and one reciprocal
+// per group instead of a division per value. Adding 1.5 * 2^23 rounds q to an integer in the
+// number's low bits, and multiplying by 2^(4 nibble) adds it into the word; what the constant's own
+// bits contribute is taken off the word's start value.
+DLLM_DEV uint32_t kv4_pack8(float (&v)[8], int& byte) {
+  float top = fabsf(v[0]);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(v[i]));   // fmaxf drops a NaN
+  for (int i = 1; i < 8; ++i) top = max_nan(top, fabsf(v[i]));
+  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  if (!(top <= 7.f * 2560.f)) {   // saturation, infinities or NaN: values brought within the codes' range first
+    top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = v[i] == v[i] ? fminf(fmaxf(v[i], -7.f * 2560.f), 7.f * 2560.f) : 0.f;
+      top = fmaxf(top, fabsf(v[i]));
+    }
+    // the neighbour took this branch too: both lanes saw the same top
+    top = fmaxf(top, __shfl_xor_sync(3u << (threadIdx.x & 30), top, 1));
+  }
   byte = kv4_scale_byte(top);
-  const float s = kv4_scale(byte);
-  uint32_t w[2] = {0x88888888u, 0x88888888u};
-  if (byte > 0) {
+  if (byte == 0) return 0x88888888u;
+  const float s = kv4_scale(byte), y = kv4_reciprocal(s);
+  const uint32_t magic = 0x4B400000u;   // 1.5 * 2^23
+  uint32_t w = 0x88888888u;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      w[h] = 0;
+  for (int i = 0; i < 8; ++i) w -= magic << (4 * (i >> 1) + 16 * (i & 1));
+  const uint64_t yy = pack_f32x2(y, y), ms = pack_f32x2(-s, -s), round = pack_f32x2(12582912.f, 12582912.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float q = fminf(fmaxf(rintf(__fdiv_rn(v[8 * h + i], s)), -7.f), 7.f);
-        const uint32_t u = v[8 * h + i] == v[8 * h + i] ? (uint32_t)((int)q + 8) : 8u;
-        w[h] |= u << (4 * (i >> 1) + 16 * (i & 1));
-      }
-    }
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t x = pack_f32x2(v[2 * i], v[2 * i + 1]);
+    const uint64_t q0 = mul_f32x2(x, yy);
+    float a, b;
+    unpack_f32x2(add_f32x2(fma_f32x2(fma_f32x2(q0, ms, x), yy, q0), round), a, b);
+    w += (__float_as_uint(a) << (4 * i)) + (__float_as_uint(b) << (4 * i + 16));
   }
-  return make_uint2(w[0], w[1]);
-}
-
-// Sixteen dims d0 .. d0 + 15 of a head at xs, rotated by cs (null: as they are).
-template <typename TI, bool VEC>
-DLLM_DEV void kv4_load16(const TI* xs, int d0, const RopeParams& r, const float2* cs, float (&v)[16]) {
-  const int half = r.rd / 2;
-  if (VEC) {
-    // rd and half are multiples of 8: each 8-dim chunk lies on one side of every border
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int d = d0 + 8 * h;
-      float a[8];
-      load8(xs + d, a);
-      if (cs != nullptr && d < r.rd) {
-        if (r.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 c = cs[d / 2 + i];
-            v[8 * h + 2 * i] = rope_first(a[2 * i], a[2 * i + 1], c);
-            v[8 * h + 2 * i + 1] = rope_second(a[2 * i], a[2 * i + 1], c);
-          }
-        } else {
-          float b[8];
-          const bool first = d < half;
-          load8(xs + (first ? d + half : d - half), b);
-          const float2* c = cs + (first ? d : d - half);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[8 * h + i] = first ? rope_first(a[i], b[i], c[i]) : rope_second(b[i], a[i], c[i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[8 * h + i] = a[i];
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int d = d0 + i;
-      const float a = load1(xs + d);
-      if (cs == nullptr || d >= r.rd) {
-        v[i] = a;
-      } else if (r.interleaved) {
-        const float b = load1(xs + (d ^ 1));
-        v[i] = d & 1 ? rope_second(b, a, cs[d >> 1]) : rope_first(a, b, cs[d >> 1]);
-      } else {
-        const bool first = d < half;
-        const float b = load1(xs + (first ? d + half : d - half));
-        v[i] = first ? rope_first(a, b, cs[d]) : rope_second(b, a, cs[d - half]);
-      }
-    }
-  }
+  return w;
 }
 
 // Appends T tokens' keys (rotated on the way) and values. One block takes `tb` tokens: their
-// cos and sin once, then one thread per 16-dim group of K or V.
-template <typename TI, bool VEC>
-__global__ void __launch_bounds__(256)
+// cos and sin once; then a thread has 8 dims (a code word) of K or V of one token after the other, two
+// neighbouring lanes a group, so that loads of 32 or 16 bytes and stores of 4 are contiguous along
+// a warp. The loads of all its tokens go out first, before the page ids (two dependent loads) and the
+// cos and sin are there; a rotated chunk's partner comes later, out of the L1 cache, where
+// another thread's load has brought it.
+template <int HD, typename TI, bool VEC>
+__global__ void __launch_bounds__(512, sizeof(TI) == 2 ? 3 : 2)
 kv4_append_kernel(const __grid_constant__ RopeParams r, Kv4 c, Kv4Addr a, const TI* __restrict__ k, long k_tok,
                   long k_head, const TI* __restrict__ v, long v_tok, long v_head,
-                  const int32_t* __restrict__ rope_pos, int T, int tb) {
-  extern __shared__ float2 cs_smem[];   // [tb][rd / 2]
+                  const int32_t* __restrict__ rope_pos, int T, TokenTiling tl) {
+  extern __shared__ float4 cs_smem[];             // [tb][rope_stride]
+  __shared__ long row_of[kMaxTokensPerBlock];     // the tokens' row in the cache (K, first head), -1: none
+  constexpr int WORDS = HD / 8;
   pdl_begin();
-  const int half = r.rd / 2;
-  const long t0 = (long)blockIdx.x * tb;
-  const int nt = (int)min((long)tb, T - t0);
-  for (int u = threadIdx.x; u < nt * half; u += blockDim.x) {
-    const int t = u / half, i = u - t * half;
-    if (a.req[t0 + t] >= 0) cs_smem[u] = rope_cos_sin(r, rope_pos[t0 + t], i);
-  }
-  __syncthreads();
-  const int groups = c.hd / 16;
-  const int per_tok = 2 * c.Hkv * groups;
-  for (int u = threadIdx.x; u < nt * per_tok; u += blockDim.x) {
-    const int t = u / per_tok;
-    int rest = u - t * per_tok;
-    const int g = rest % groups;
-    rest /= groups;
-    const int kv = rest / c.Hkv, h = rest - kv * c.Hkv;
-    int off;
-    const int id = kv4_page_of(c, a, t0 + t, off);
-    if (id < 0) continue;
-    float x[16];
-    if (kv == 0)
-      kv4_load16<TI, VEC>(k + (t0 + t) * k_tok + h * k_head, 16 * g, r, r.rd > 0 ? cs_smem + t * half : nullptr, x);
-    else
-      kv4_load16<TI, VEC>(v + (t0 + t) * v_tok + h * v_head, 16 * g, r, nullptr, x);
-    int byte;
-    const uint2 w = kv4_pack(x, byte);
-    const long row = kv4_row(c, id, kv, h, off);
-    *reinterpret_cast<uint2*>(c.codes + row * (c.hd / 2) + 8 * g) = w;
-    c.scales[row * (c.hd / 16) + g] = (uint8_t)byte;
+  const int half = r.rd / 2, stride = rope_stride(r.rd);
+  const long t0 = (long)blockIdx.x * tl.tb;
+  const int nt = (int)min((long)tl.tb, T - t0);
+  // lanes past the last word go along with it, since neighbours talk to each other
+  const int tl0 = tl.tp > 1 ? min((int)threadIdx.x / tl.units, tl.tp - 1) : 0;
+  for (int base = 0; base < tl.units; base += blockDim.x) {
+    const int mine = threadIdx.x - tl0 * tl.units + base;
+    const int unit = min(mine, tl.units - 2 + (mine & 1));
+    const int row = unit / WORDS, w = unit - row * WORDS;     // row: K heads, then V heads
+    const int d = 8 * w;
+    const bool is_k = row < c.Hkv;
+    const long x_step = tl.tp * (is_k ? k_tok : v_tok);
+    const TI* xs = (is_k ? k + (t0 + tl0) * k_tok + row * k_head : v + (t0 + tl0) * v_tok + (row - c.Hkv) * v_head) + d;
+    const bool rot = is_k && d < r.rd, pair = rot && !r.interleaved;
+    const bool first = d < half;
+    const int away = first ? half : -half;
+    const int q0 = pair ? (first ? d : d - half) / 2 : d / 4;
+    const uint32_t flip = first ? 0x80000000u : 0u;           // a cos - b sin in the first half, b cos + a sin in the second
+    uint8_t* codes = c.codes + ((long)row << c.page_shift) * (HD / 2) + 4 * w;      // V's heads follow K's
+    uint8_t* scales = c.scales + ((long)row << c.page_shift) * (HD / 16) + w / 2;
+    const float4* cs = cs_smem + tl0 * stride;
+    Raw8<TI> next;
+    if (VEC && tl0 < nt) next.load(xs);
+    if (base == 0) {
+      for (int t = threadIdx.x; t < nt; t += blockDim.x) {
+        int off = 0;
+        const int id = kv4_page_of(c, a, t0 + t, off);
+        row_of[t] = id < 0 ? -1 : kv4_row(c, id, 0, 0, off);
+      }
+      rope_fill(r, rope_pos, t0, nt, cs_smem);
+      __syncthreads();
+    }
+    for (int step = 0; step < nt; step += tl.tp) {            // the same for the whole block
+      const int t = tl0 + step;
+      const long at = t < nt ? row_of[t] : -1;
+      const Raw8<TI> raw = next;
+      if (VEC && t + tl.tp < nt) next.load(xs + x_step);
+      float x[8];
+      if (at < 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+      } else if (VEC) {
+        raw.get(x);
+        if (pair) {
+          Raw8<TI> xb;
+          float y[8];
+          xb.load(xs + away);
+          xb.flip(flip);
+          xb.get(y);
+          rope_turn8<0>(x, y, cs, q0);
+        } else if (rot) {
+          rope_turn4(x, cs, q0);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int dd = d + e;
+          const float own = load1(xs + e);
+          if (!is_k || dd >= r.rd) {
+            x[e] = own;
+          } else if (r.interleaved) {
+            const float2 q = rope_pair(cs, dd >> 1);
+            const float other = load1(xs + (dd & 1 ? e - 1 : e + 1));
+            x[e] = dd & 1 ? rope_second(other, own, q) : rope_first(own, other, q);
+          } else {
+            const bool lo = dd < half;
+            const float2 q = rope_pair(cs, lo ? dd : dd - half);
+            const float other = load1(xs + e + (lo ? half : -half));
+            x[e] = lo ? rope_first(own, other, q) : rope_second(other, own, q);
+          }
+        }
+      }
+      int byte;
+      const uint32_t word = kv4_pack8(x, byte);
+      if (at >= 0 && mine < tl.units) {
+        *reinterpret_cast<uint32_t*>(codes + at * (HD / 2)) = word;
+        if ((w & 1) == 0) scales[at * (HD / 16)] = (uint8_t)byte;
+      }
+      xs += x_step;
+      cs += tl.tp * stride;
+    }
   }
 }
 
@@ -201,43 +245,58 @@ DLLM_DEV __nv_bfloat162 kv4_scale_bf16x2(uint32_t byte) {
   return __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), *reinterpret_cast<const __nv_bfloat162*>(&up));
 }
 
-// Reads T tokens' rows back as bf16 [T][Hkv][hd]: one thread per 16-dim group. A token
-// with no page reads NaN; a padding token's rows stay as they are.
+// Reads T tokens' rows back as bf16 [T][Hkv][hd]. One warp per token, lanes along its groups of 16
+// dims (K's heads, then V's), whose loads are all issued before the first is used. A token with no
+// page reads NaN; a padding token's rows are zeroed or left as they are.
+template <int HD>
 __global__ void __launch_bounds__(256)
-kv4_read_kernel(Kv4 c, Kv4Addr a, long T, bf16_t* __restrict__ k_out, bf16_t* __restrict__ v_out) {
+kv4_read_kernel(Kv4 c, Kv4Addr a, int T, bf16_t* __restrict__ k_out, bf16_t* __restrict__ v_out, int zero_padding) {
+  constexpr int G = HD / 16, UNROLL = 6;
   pdl_begin();
-  const int groups = c.hd / 16;
-  const long per_kv = T * c.Hkv * groups;
-  const long u = (long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (u >= per_kv) return;
-  const int kv = blockIdx.y;
-  bf16_t* out = kv ? v_out : k_out;
-  if (out == nullptr) return;
-  const long row_out = u / groups;
-  const int g = (int)(u - row_out * groups);
-  const long t = row_out / c.Hkv;
-  const int h = (int)(row_out - t * c.Hkv);
+  const long t = (long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (t >= T) return;
+  const int lane = threadIdx.x & 31;
   int off = 0;
   const int id = kv4_page_of(c, a, t, off);
-  if (id == -2) return;
-  uint32_t o[8];
-  if (id < 0) {
+  if (id == -2 && !zero_padding) return;
+  const int per_kv = c.Hkv * G;
+  const int first = k_out != nullptr ? 0 : per_kv, last = v_out != nullptr ? 2 * per_kv : per_kv;
+  const long row0 = id >= 0 ? kv4_row(c, id, 0, 0, off) : 0;
+  for (int u0 = first + lane; u0 < last; u0 += 32 * UNROLL) {
+    uint2 w[UNROLL];
+    uint32_t b[UNROLL];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = 0x7FC07FC0u;
-  } else {
-    const long row = kv4_row(c, id, kv, h, off);
-    const uint2 w = *reinterpret_cast<const uint2*>(c.codes + row * (c.hd / 2) + 8 * g);
-    const __nv_bfloat162 s = kv4_scale_bf16x2(c.scales[row * (c.hd / 16) + g]);
-    const __nv_bfloat162 ms24 = __hmul2(s, __float2bfloat162_rn(-24.f));
+    for (int i = 0; i < UNROLL; ++i) {
+      const int u = u0 + 32 * i;
+      if (u < last && id >= 0) {
+        const int h = u / G, g = u - h * G;              // V's heads follow K's
+        const long row = row0 + ((long)h << c.page_shift);
+        w[i] = *reinterpret_cast<const uint2*>(c.codes + row * (HD / 2) + 8 * g);
+        b[i] = c.scales[row * (HD / 16) + g];
+      }
+    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      o[j] = kv4_bf16x2(w.x, j, s, ms24);
-      o[4 + j] = kv4_bf16x2(w.y, j, s, ms24);
+    for (int i = 0; i < UNROLL; ++i) {
+      const int u = u0 + 32 * i;
+      if (u >= last) continue;
+      uint32_t o[8];
+      if (id < 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = id == -1 ? 0x7FC07FC0u : 0u;
+      } else {
+        const __nv_bfloat162 s = kv4_scale_bf16x2(b[i]);
+        const __nv_bfloat162 ms24 = __hmul2(s, __float2bfloat162_rn(-24.f));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          o[j] = kv4_bf16x2(w[i].x, j, s, ms24);
+          o[4 + j] = kv4_bf16x2(w[i].y, j, s, ms24);
+        }
+      }
+      bf16_t* out = u < per_kv ? k_out + t * (c.Hkv * HD) + u * 16 : v_out + t * (c.Hkv * HD) + (u - per_kv) * 16;
+      reinterpret_cast<uint4*>(out)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<uint4*>(out)[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
   }
-  uint4* dst = reinterpret_cast<uint4*>(out + row_out * c.hd + 16 * g);
-  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 }  // namespace dllm

@@ -202,17 +202,19 @@ class KVCache4:
         """Positions pos of table rows req as bf16 (k, v), each [T][n_kv_heads][head_dim]. Rows of padding
         (req < 0) are left as they were in k_out and v_out, and are zero in outputs made here."""
         T, H, d, dev = req.shape[0], self.n_kv_heads, self.head_dim, self._dev
-        outs = []
+        outs, made = [], k_out is None or v_out is None
+        if made and not (k_out is None and v_out is None):
+            _bad("k_out, v_out", "give both or neither")
         for name, t in (("k_out", k_out), ("v_out", v_out)):
             if t is None:
-                t = self.codes.new_zeros((T, H, d), dtype=torch.bfloat16)
+                t = self.codes.new_empty((T, H, d), dtype=torch.bfloat16)
             else:
                 _heads(name, t, dev, T, H, d, (torch.bfloat16,))
                 if not t.is_contiguous():
                     _bad(name, "has to be contiguous")
             outs.append(t)
         _launch(dev, binding.dllm_op_read_kv4, self.c, _ints("req", req, dev, T), _ints("pos", pos, dev, T), T,
-                *_table(table, dev), outs[0].data_ptr(), outs[1].data_ptr())
+                *_table(table, dev), outs[0].data_ptr(), outs[1].data_ptr(), 1 if made else 0)
         return outs[0], outs[1]
 
     def attend(self, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor, max_q: int,

@@ -97,7 +97,7 @@ P = 1 << 22   # stands for a device address: a refused call never reads it
 def test_every_operation_refuses_a_bad_cache(lib, bad):
     c = _cache(**bad)
     assert lib.dllm_op_append_kv4(c, P, 128, 64, P, 128, 64, 0, P, P, None, 4, P, 1, 1, None, None) == binding.DLLM_E_INVAL
-    assert lib.dllm_op_read_kv4(c, P, P, 4, P, 1, 1, P, P, None) == binding.DLLM_E_INVAL
+    assert lib.dllm_op_read_kv4(c, P, P, 4, P, 1, 1, P, P, 0, None) == binding.DLLM_E_INVAL
     assert lib.dllm_op_attn_kv4_workspace(c, 1, 1, 1, 64, 2) == binding.DLLM_E_INVAL
     assert lib.dllm_op_attn_kv4(c, P, 128, 64, P, 128, 64, None, P, P, 1, 1, 1, 64, 2, P, 1, 0, 1.0, None, 0,
                                 None) == binding.DLLM_E_INVAL
@@ -116,16 +116,16 @@ def test_append_and_read_refuse(lib):
                 dict(v=P + 8)):
         a = {**ok, **bad}
         assert lib.dllm_op_read_kv4(c, a["req"], a["pos"], a["T"], a["table"], a["n_req"], a["stride"], a["k"], a["v"],
-                                    None) == binding.DLLM_E_INVAL, bad
+                                    0, None) == binding.DLLM_E_INVAL, bad
     # nothing to do is not an error, and queues nothing
     assert lib.dllm_op_append_kv4(c, None, 0, 0, None, 0, 0, 0, None, None, None, 0, None, 0, 0, None, None) == 0
-    assert lib.dllm_op_read_kv4(c, None, None, 0, None, 0, 0, None, None, None) == 0
+    assert lib.dllm_op_read_kv4(c, None, None, 0, None, 0, 0, None, None, 0, None) == 0
 
 
 def test_rope_refuses(lib):
     ok = dict(rope=Rope(64).c, x=P, xt=0, pos=P, T=4, H=2, hd=64, y=2 * P, yt=0, ys=64)
-    for bad in (dict(rope=None), dict(x=None), dict(y=None), dict(pos=None), dict(xt=2), dict(yt=-1), dict(T=-1), dict(H=0),
-                dict(hd=62), dict(hd=2048), dict(y=P, yt=1), dict(y=P, ys=128)):
+    for bad in (dict(rope=None), dict(x=None), dict(y=None), dict(pos=None), dict(xt=2), dict(yt=-1), dict(T=-1), dict(H=0), dict(H=32769),
+                dict(H=16385), dict(hd=62), dict(hd=2048), dict(y=P, yt=1), dict(y=P, ys=128)):
         a = {**ok, **bad}
         assert lib.dllm_op_rope(a["rope"], a["x"], a["xt"], 128, 64, a["pos"], a["T"], a["H"], a["hd"], a["y"], a["yt"], 128,
                                 a["ys"], 0, None) == binding.DLLM_E_INVAL, bad
