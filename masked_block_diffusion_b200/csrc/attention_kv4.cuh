@@ -11,8 +11,12 @@
 // fills the 16-row side of mma.m16n8k16 and eight query rows its 8-column side. (The 5th-
 // generation tensor instruction reads its operands from shared or tensor memory only; with
 // rows this few, writing the unpacked values there and reading them back would cost more
-// than the multiplication.) Unpacking is an AND, an OR and one exact fma per two values plus
-// a shift. Thread (r, c) = (lane / 4, lane % 4):
+// than the multiplication.) Unpacking is what costs, mostly on the integer pipe: per word of eight
+// codes two shifts, four AND-ORs and four exact fmas (kv4_sixteenth). Both operands are unpacked to
+// sixteenths of their values in fp16, for which two nibbles need one shift; Q goes to fp16 with a
+// power of two per row that keeps its largest value near the top of the range (a bf16 value
+// has 8 bits, fp16 11, so only values 2^-28 of the row's largest lose any). Thread (r, c) =
+// (lane / 4, lane % 4):
 //   K: token r's and token r + 8's dims 64 i + 16 c .. + 15 (8 code bytes and their scale) are
 //      its A fragments of four k16 steps; Q's fragments carry the same dims.
 //   V: tokens 2c, 2c + 1, 2c + 8, 2c + 9, dims 8 w .. 8 w + 7 with w = 8 i + r: a byte permute
@@ -115,6 +119,32 @@ DLLM_DEV uint32_t kv4_f16x2(uint32_t w, int j, __half2 s, __half2 ms24) {
 
 DLLM_DEV __half2 kv4_half2(uint32_t bits) { return *reinterpret_cast<const __half2*>(&bits); }
 
+// The four nibble pairs of a code word as sixteenths, pair j holding dims 2 j and 2 j + 1 (or two keys'
+// same dim). A nibble u at bits 2..5 of an fp16 number of exponent 2^4 is 16 + u / 16, at bits 6..9
+// of one of exponent 2^0 it is 1 + u / 16, so one shift serves two neighbouring nibbles; then
+// (16 + u / 16) s - 16.5 s = (u - 8) s / 16, and likewise with 1.5 s: exact, since 16.5 s and 1.5 s
+// have at most 10 bits and the fma rounds once (scales up to 2560: 16.5 s < 65504).
+struct Kv4Scale2 {
+  __half2 s, m16, m1;   // the scale, -16.5 and -1.5 times it
+};
+DLLM_DEV Kv4Scale2 kv4_scale2(uint32_t bits) {
+  Kv4Scale2 r;
+  r.s = kv4_half2(bits);
+  r.m16 = __hmul2(r.s, __float2half2_rn(-16.5f));
+  r.m1 = __hmul2(r.s, __float2half2_rn(-1.5f));
+  return r;
+}
+DLLM_DEV void kv4_sixteenth(uint32_t w, const Kv4Scale2& s, uint32_t (&o)[4]) {
+  const uint32_t a = w * 4, b = w >> 6;   // (bits of the other half that a shift brings along are masked)
+  const uint32_t u[4] = {(a & 0x003C003Cu) | 0x4C004C00u, (a & 0x03C003C0u) | 0x3C003C00u,
+                         (b & 0x003C003Cu) | 0x4C004C00u, (b & 0x03C003C0u) | 0x3C003C00u};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __half2 v = __hfma2(kv4_half2(u[j]), s.s, j & 1 ? s.m1 : s.m16);
+    o[j] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
 // Shared memory of a block: `STAGES` stages of 64 keys' packed K and V; four consumer warps
 // take 16 keys each, a fifth warp issues the copies. 48 KB or less, so that several blocks
 // share an SM and keep enough bytes in flight.
@@ -216,8 +246,9 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
   } else {
     // ---------------- consumers
     const int r = lane >> 2, c = lane & 3;
-    uint32_t qf[NR][KI][8];
+    uint32_t qf[NR][KI][8];               // fp16, scaled by a power of two per row
     int lim[NR][2];                       // columns 2c, 2c + 1: keys the row sees end here
+    float fac[NR][2];                     // and what turns their sums into log2 weights
     float m[NR][2], l[NR][2];
     float o[NR][KI][4][4];
 #pragma unroll
@@ -237,10 +268,31 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
           qf[nr][i][4 * h + 2] = v.z;
           qf[nr][i][4 * h + 3] = v.w;
         }
+      // the row's largest magnitude to [2^14, 2^15): bf16 bits compare like their magnitudes
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < KI; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, max(qf[nr][i][e] & 0x7FFFu, (qf[nr][i][e] >> 16) & 0x7FFFu));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // exponent field e: times 2^(141 - e), in two factors that are normal numbers for every e
+      const int up = 141 - max((int)(top >> 7), 15);          // -114 .. 126
+      const float scale_q = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+      for (int i = 0; i < KI; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const __half2 v = __floats2half2_rn(__uint_as_float(qf[nr][i][e] << 16) * scale_q,
+                                              __uint_as_float(qf[nr][i][e] & 0xFFFF0000u) * scale_q);
+          qf[nr][i][e] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+      const float down = __uint_as_float((uint32_t)(127 - up) << 23);   // 2^-up: normal
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int Rc = R0 + 8 * nr + 2 * c + e;
         lim[nr][e] = Rc < n_rows ? min(ke, kv4_row_limit(p, rq, Rc / p.group)) : 0;
+        fac[nr][e] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + e)) * 16.f * p.scale_log2;
         m[nr][e] = -INFINITY;
         l[nr][e] = 0.f;
       }
@@ -252,6 +304,8 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
           for (int e = 0; e < 4; ++e) o[nr][i][j][e] = 0.f;
     }
 
+    const int all_see = min(ke, kv4_row_limit(p, rq, R0 / p.group));   // every row of the tile sees the keys below
+    const bool rows_full = R0 + G::kRows <= n_rows;
     bool ok = true;
     for (int it = 0; it < nst; ++it) {
       const int st = it % G::STAGES;
@@ -270,7 +324,7 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
           const int grp = 4 * i + c;
-          const bool in = 16 * grp < HD;
+          const bool in = 64 * (i + 1) <= HD || 16 * grp < HD;
           uint2 wa = make_uint2(0, 0), wb = wa;
           uint32_t ba = 0, bb = 0;
           if (in) {
@@ -279,19 +333,18 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
             ba = kS[r * (HD / 16) + grp];
             bb = kS[(r + 8) * (HD / 16) + grp];
           }
-          const __nv_bfloat162 m24 = __float2bfloat162_rn(-24.f);
-          const __nv_bfloat162 sa = kv4_scale_bf16x2(ba), sb = kv4_scale_bf16x2(bb);
-          const __nv_bfloat162 na = __hmul2(sa, m24), nb = __hmul2(sb, m24);
+          const Kv4Scale2 sa = kv4_scale2(ba * 0x00800080u), sb = kv4_scale2(bb * 0x00800080u);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t xa = h ? wa.y : wa.x, xb = h ? wb.y : wb.x;
+            uint32_t xa[4], xb[4];
+            kv4_sixteenth(h ? wa.y : wa.x, sa, xa);
+            kv4_sixteenth(h ? wb.y : wb.x, sb, xb);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const uint32_t a[4] = {kv4_bf16x2(xa, 2 * k, sa, na), kv4_bf16x2(xb, 2 * k, sb, nb),
-                                     kv4_bf16x2(xa, 2 * k + 1, sa, na), kv4_bf16x2(xb, 2 * k + 1, sb, nb)};
+              const uint32_t a[4] = {xa[2 * k], xb[2 * k], xa[2 * k + 1], xb[2 * k + 1]};
 #pragma unroll
               for (int nr = 0; nr < NR; ++nr)
-                mma_bf16_16816(s[nr], a, qf[nr][i][4 * h + 2 * k], qf[nr][i][4 * h + 2 * k + 1]);
+                mma_f16_16816(s[nr], a, qf[nr][i][4 * h + 2 * k], qf[nr][i][4 * h + 2 * k + 1]);
             }
           }
         }
@@ -299,9 +352,11 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[nr][e] *= p.scale_log2;
-            if (t0 + r + 8 * (e >> 1) >= lim[nr][e & 1]) s[nr][e] = -INFINITY;
+          for (int e = 0; e < 4; ++e) s[nr][e] *= fac[nr][e & 1];
+          if (t0 + 16 > all_see || !rows_full) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (t0 + r + 8 * (e >> 1) >= lim[nr][e & 1]) s[nr][e] = -INFINITY;
           }
           const float mx0 = fmaxf(s[nr][0], s[nr][2]), mx1 = fmaxf(s[nr][1], s[nr][3]);
           // a new reference only when a score is more than 2^14 above it (the first visible key always is)
@@ -338,28 +393,30 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
           const int w = 8 * i + r;
-          const bool in = w < WORDS;
-          uint32_t x[4], sc[4];
+          const bool in = 8 * (i + 1) <= WORDS || w < WORDS;
+          uint32_t x[4] = {0, 0, 0, 0}, sc[4] = {0, 0, 0, 0};
+          if (in) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int t = 2 * c + (e & 1) + 8 * (e >> 1);
-            x[e] = 0;
-            sc[e] = 0;
-            if (in) {
+            for (int e = 0; e < 4; ++e) {
+              const int t = 2 * c + (e & 1) + 8 * (e >> 1);
               x[e] = *reinterpret_cast<const uint32_t*>(vc + t * (HD / 2) + 4 * w);
               sc[e] = vS[t * (HD / 16) + w / 2];
             }
-            if (tail && t0 + t >= ke) sc[e] = 0;
           }
-          const __half2 m24 = __float2half2_rn(-24.f);
-          const __half2 s0 = kv4_half2((sc[0] << 7) | (sc[1] << 23)), s1 = kv4_half2((sc[2] << 7) | (sc[3] << 23));
-          const __half2 n0 = __hmul2(s0, m24), n1 = __hmul2(s1, m24);
-          const uint32_t e0 = __byte_perm(x[0], x[1], 0x5410), d0 = __byte_perm(x[0], x[1], 0x7632);
-          const uint32_t e1 = __byte_perm(x[2], x[3], 0x5410), d1 = __byte_perm(x[2], x[3], 0x7632);
+          if (tail) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (t0 + 2 * c + (e & 1) + 8 * (e >> 1) >= ke) sc[e] = 0;
+          }
+          const Kv4Scale2 s0 = kv4_scale2((sc[1] * 65536u + sc[0]) * 128u), s1 = kv4_scale2((sc[3] * 65536u + sc[2]) * 128u);
+          uint32_t e0[4], d0[4], e1[4], d1[4];   // even and odd dims of the two pairs of tokens
+          kv4_sixteenth(__byte_perm(x[0], x[1], 0x5410), s0, e0);
+          kv4_sixteenth(__byte_perm(x[0], x[1], 0x7632), s0, d0);
+          kv4_sixteenth(__byte_perm(x[2], x[3], 0x5410), s1, e1);
+          kv4_sixteenth(__byte_perm(x[2], x[3], 0x7632), s1, d1);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t a[4] = {kv4_f16x2(e0, j, s0, n0), kv4_f16x2(d0, j, s0, n0), kv4_f16x2(e1, j, s1, n1),
-                                   kv4_f16x2(d1, j, s1, n1)};
+            const uint32_t a[4] = {e0[j], d0[j], e1[j], d1[j]};
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) mma_f16_16816(o[nr][i][j], a, pf[nr][0], pf[nr][1]);
           }
@@ -418,7 +475,7 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
       a0 += f * row[d];
       a1 += f * row[d + 1];
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : 16.f / sum;   // V came in sixteenths
     float lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);
     a0 *= inv;
     a1 *= inv;
