@@ -50,6 +50,7 @@ struct AttnKv4Params {
   float scale_log2;         // scale * log2(e)
   float* part_o;            // [n_splits][T][H][hd]
   float* part_lse;          // [n_splits][T][H], log2 domain
+  uint32_t mask_low, mask_high;   // Kv4Masks
 };
 
 // A request's queries and keys. bad: its row range holds, but not its lengths: every row becomes NaN.
@@ -127,6 +128,17 @@ DLLM_DEV __half2 kv4_half2(uint32_t bits) { return *reinterpret_cast<const __hal
 struct Kv4Scale2 {
   __half2 s, m16, m1;   // the scale, -16.5 and -1.5 times it
 };
+// (a & mask) | bits in one operation. An instruction takes one constant: the masks come as kernel
+// parameters, which the compiler keeps in registers, where with two constants it splits the operation.
+template <uint32_t BITS>
+DLLM_DEV uint32_t and_or(uint32_t a, uint32_t mask) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "n"(BITS));
+  return d;
+}
+struct Kv4Masks {
+  uint32_t low, high;   // 0x003C003C, 0x03C003C0
+};
 DLLM_DEV Kv4Scale2 kv4_scale2(uint32_t bits) {
   Kv4Scale2 r;
   r.s = kv4_half2(bits);
@@ -134,10 +146,10 @@ DLLM_DEV Kv4Scale2 kv4_scale2(uint32_t bits) {
   r.m1 = __hmul2(r.s, __float2half2_rn(-1.5f));
   return r;
 }
-DLLM_DEV void kv4_sixteenth(uint32_t w, const Kv4Scale2& s, uint32_t (&o)[4]) {
+DLLM_DEV void kv4_sixteenth(uint32_t w, const Kv4Scale2& s, const Kv4Masks& m, uint32_t (&o)[4]) {
   const uint32_t a = w * 4, b = w >> 6;   // (bits of the other half that a shift brings along are masked)
-  const uint32_t u[4] = {(a & 0x003C003Cu) | 0x4C004C00u, (a & 0x03C003C0u) | 0x3C003C00u,
-                         (b & 0x003C003Cu) | 0x4C004C00u, (b & 0x03C003C0u) | 0x3C003C00u};
+  const uint32_t u[4] = {and_or<0x4C004C00u>(a, m.low), and_or<0x3C003C00u>(a, m.high), and_or<0x4C004C00u>(b, m.low),
+                         and_or<0x3C003C00u>(b, m.high)};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const __half2 v = __hfma2(kv4_half2(u[j]), s.s, j & 1 ? s.m1 : s.m16);
@@ -306,6 +318,7 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
 
     const int all_see = min(ke, kv4_row_limit(p, rq, R0 / p.group));   // every row of the tile sees the keys below
     const bool rows_full = R0 + G::kRows <= n_rows;
+    const Kv4Masks masks{p.mask_low, p.mask_high};
     bool ok = true;
     for (int it = 0; it < nst; ++it) {
       const int st = it % G::STAGES;
@@ -337,8 +350,8 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t xa[4], xb[4];
-            kv4_sixteenth(h ? wa.y : wa.x, sa, xa);
-            kv4_sixteenth(h ? wb.y : wb.x, sb, xb);
+            kv4_sixteenth(h ? wa.y : wa.x, sa, masks, xa);
+            kv4_sixteenth(h ? wb.y : wb.x, sb, masks, xb);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const uint32_t a[4] = {xa[2 * k], xb[2 * k], xa[2 * k + 1], xb[2 * k + 1]};
@@ -410,10 +423,10 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
           }
           const Kv4Scale2 s0 = kv4_scale2((sc[1] * 65536u + sc[0]) * 128u), s1 = kv4_scale2((sc[3] * 65536u + sc[2]) * 128u);
           uint32_t e0[4], d0[4], e1[4], d1[4];   // even and odd dims of the two pairs of tokens
-          kv4_sixteenth(__byte_perm(x[0], x[1], 0x5410), s0, e0);
-          kv4_sixteenth(__byte_perm(x[0], x[1], 0x7632), s0, d0);
-          kv4_sixteenth(__byte_perm(x[2], x[3], 0x5410), s1, e1);
-          kv4_sixteenth(__byte_perm(x[2], x[3], 0x7632), s1, d1);
+          kv4_sixteenth(__byte_perm(x[0], x[1], 0x5410), s0, masks, e0);
+          kv4_sixteenth(__byte_perm(x[0], x[1], 0x7632), s0, masks, d0);
+          kv4_sixteenth(__byte_perm(x[2], x[3], 0x5410), s1, masks, e1);
+          kv4_sixteenth(__byte_perm(x[2], x[3], 0x7632), s1, masks, d1);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t a[4] = {e0[j], d0[j], e1[j], d1[j]};

@@ -348,6 +348,8 @@ int dllm_op_attn_kv4(const dllm_kv4* cache, const uint16_t* q, long long q_token
   p.n_splits = a.n_splits;
   p.chunk = a.chunk;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.mask_low = 0x003C003Cu;
+  p.mask_high = 0x03C003C0u;
   p.part_o = reinterpret_cast<float*>(workspace);
   p.part_lse = p.part_o + (size_t)a.n_splits * T * H * cache->head_dim;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
