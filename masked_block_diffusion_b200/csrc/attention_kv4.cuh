@@ -157,32 +157,36 @@ DLLM_DEV void kv4_sixteenth(uint32_t w, const Kv4Scale2& s, const Kv4Masks& m, u
   }
 }
 
-// Shared memory of a block: `STAGES` stages of 64 keys' packed K and V; four consumer warps
-// take 16 keys each, a fifth warp issues the copies. 48 KB or less, so that several blocks
-// share an SM and keep enough bytes in flight.
+// Shared memory of a block: `STAGES` stages of 128 keys' packed K and V, 32 keys for each of four
+// warps. Each warp has two 16-key tiles under way at a time, which are independent until the products
+// with V. The first warp also issues the copies, so that no warp's registers are spent on that
+// alone and four blocks of one 8-row column share an SM; they hold 100 KB of copies in flight.
 template <int HD, int NR>
 struct AttnKv4Cfg {
-  static constexpr int KEYS = 64;
+  static constexpr int KEYS = 128;
   static constexpr int WARPS = 4;
+  static constexpr int TILES = KEYS / WARPS / 16;
   static constexpr int kCodes = KEYS * HD / 2;
   static constexpr int kScales = KEYS * HD / 16;
   static constexpr int kStage = 2 * (kCodes + kScales);
-  static constexpr int STAGES = HD == 64 ? 8 : 4;
+  static constexpr int STAGES = HD == 64 ? 4 : 2;
   static constexpr int kRows = 8 * NR;
   static constexpr int kRed = WARPS * kRows * (HD + 2) * 4;     // the warps' results, over the stages
   static constexpr int kBody = STAGES * kStage > kRed ? STAGES * kStage : kRed;
   static constexpr int kOffBar = (kBody + 15) / 16 * 16;
   static constexpr int kTotal = kOffBar + 2 * STAGES * 8 + 16;
-  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int BLOCKS = NR == 1 ? 4 : HD == 176 ? 2 : 3;   // per SM
 };
 
 // Grid (n_splits, Hkv * row tiles, B). A block takes 8 NR rows of one KV head over one split.
 template <int HD, int NR>
-__global__ void __launch_bounds__(AttnKv4Cfg<HD, NR>::THREADS, NR == 1 ? 3 : 2)
+__global__ void __launch_bounds__(AttnKv4Cfg<HD, NR>::THREADS, AttnKv4Cfg<HD, NR>::BLOCKS)
 attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
   using G = AttnKv4Cfg<HD, NR>;
   constexpr int KI = (HD + 63) / 64;
   constexpr int WORDS = HD / 8;
+  constexpr int TI = G::TILES;
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);
   uint64_t* empty = full + G::STAGES;
@@ -214,137 +218,143 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
   }
   __syncthreads();
 
-  if (warp == G::WARPS) {
-    // ---------------- producer: lane i copies piece i of a stage (a page's share of it)
-    const int shift = min(p.c.page_shift, 6);
-    const int pieces = G::KEYS >> shift, keys = 1 << shift;
-    const uint32_t codes = keys * HD / 2, scales = keys * HD / 16;
-    const int* row = p.table + (long)b * p.stride;
-    bool ok = true;
-    int it = 0;
-    for (; it < nst; ++it) {
-      const int t = ks + it * G::KEYS + lane * keys;
-      int id = -1;
-      const bool want = lane < pieces && t < ke;
-      if (want) {
-        id = row[t >> p.c.page_shift];
-        if (id < 0 || id >= p.c.n_pages) {
-          id = -1;
-          flags[1] = 1;
-        }
-      }
-      const uint32_t n = __popc(__ballot_sync(0xffffffffu, id >= 0));
-      const int st = it % G::STAGES;
-      if (!mbar_wait(&empty[st], ((it / G::STAGES) & 1) ^ 1, flags)) ok = false;
-      if (!__all_sync(0xffffffffu, ok)) break;
-      if (lane == 0) mbar_arrive_expect_tx(&full[st], n * 2 * (codes + scales));
-      __syncwarp();
-      if (id >= 0) {
-        uint8_t* dst = smem + st * G::kStage;
-        const int off = t & ((1 << p.c.page_shift) - 1);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const long r = kv4_row(p.c, id, kv, g, off);
-          uint8_t* d = dst + kv * (G::kCodes + G::kScales);
-          bulk_load(d + lane * codes, p.c.codes + r * (HD / 2), codes, &full[st]);
-          bulk_load(d + G::kCodes + lane * scales, p.c.scales + r * (HD / 16), scales, &full[st]);
-        }
+  // Copies stage `it` (first warp): lane i takes piece i, a page's share of it. False if its stage did
+  // not come free.
+  auto copy_stage = [&](int it) -> bool {
+    const int shift = min(p.c.page_shift, 7);
+    const int keys = 1 << shift;
+    const int t = ks + it * G::KEYS + lane * keys;
+    int id = -1;
+    if (lane < (G::KEYS >> shift) && t < ke) {
+      id = p.table[(long)b * p.stride + (t >> p.c.page_shift)];
+      if (id < 0 || id >= p.c.n_pages) {
+        id = -1;
+        flags[1] = 1;
       }
     }
-    if (!__all_sync(0xffffffffu, ok)) flags[0] = 1;
-    // whatever the consumers did, the copies already issued land before the stages are used otherwise
-    for (int j = max(0, it - G::STAGES); j < it; ++j) mbar_drain(&full[j % G::STAGES], (j / G::STAGES) & 1);
-    __syncthreads();
-  } else {
-    // ---------------- consumers
-    const int r = lane >> 2, c = lane & 3;
-    uint32_t qf[NR][KI][8];               // fp16, scaled by a power of two per row
-    int lim[NR][2];                       // columns 2c, 2c + 1: keys the row sees end here
-    float fac[NR][2];                     // and what turns their sums into log2 weights
-    float m[NR][2], l[NR][2];
-    float o[NR][KI][4][4];
+    const uint32_t codes = keys * (HD / 2), scales = keys * (HD / 16);
+    const uint32_t n = __popc(__ballot_sync(0xffffffffu, id >= 0));
+    const int st = it % G::STAGES;
+    if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ((it / G::STAGES) & 1) ^ 1, flags))) return false;
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], n * 2 * (codes + scales));
+    __syncwarp();
+    if (id >= 0) {
+      uint8_t* dst = smem + st * G::kStage;
+      const int off = t & ((1 << p.c.page_shift) - 1);
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
-      const int R = R0 + 8 * nr + r;
-      const bool real = R < n_rows;
-      const bf16_t* qr = p.q + (long)(rq.q0 + (real ? R / p.group : 0)) * p.q_tok + (g * p.group + (real ? R % p.group : 0)) * p.q_head;
-#pragma unroll
-      for (int i = 0; i < KI; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int d = 64 * i + 16 * c + 8 * h;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (real && d < HD) v = *reinterpret_cast<const uint4*>(qr + d);
-          qf[nr][i][4 * h] = v.x;
-          qf[nr][i][4 * h + 1] = v.y;
-          qf[nr][i][4 * h + 2] = v.z;
-          qf[nr][i][4 * h + 3] = v.w;
-        }
-      // the row's largest magnitude to [2^14, 2^15): bf16 bits compare like their magnitudes
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < KI; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, max(qf[nr][i][e] & 0x7FFFu, (qf[nr][i][e] >> 16) & 0x7FFFu));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // exponent field e: times 2^(141 - e), in two factors that are normal numbers for every e
-      const int up = 141 - max((int)(top >> 7), 15);          // -114 .. 126
-      const float scale_q = __uint_as_float((uint32_t)(127 + up) << 23);
-#pragma unroll
-      for (int i = 0; i < KI; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const __half2 v = __floats2half2_rn(__uint_as_float(qf[nr][i][e] << 16) * scale_q,
-                                              __uint_as_float(qf[nr][i][e] & 0xFFFF0000u) * scale_q);
-          qf[nr][i][e] = *reinterpret_cast<const uint32_t*>(&v);
-        }
-      const float down = __uint_as_float((uint32_t)(127 - up) << 23);   // 2^-up: normal
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int Rc = R0 + 8 * nr + 2 * c + e;
-        lim[nr][e] = Rc < n_rows ? min(ke, kv4_row_limit(p, rq, Rc / p.group)) : 0;
-        fac[nr][e] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + e)) * 16.f * p.scale_log2;
-        m[nr][e] = -INFINITY;
-        l[nr][e] = 0.f;
+      for (int kv = 0; kv < 2; ++kv) {
+        const long r = kv4_row(p.c, id, kv, g, off);
+        uint8_t* d = dst + kv * (G::kCodes + G::kScales);
+        bulk_load(d + lane * codes, p.c.codes + r * (HD / 2), codes, &full[st]);
+        bulk_load(d + G::kCodes + lane * scales, p.c.scales + r * (HD / 16), scales, &full[st]);
       }
-#pragma unroll
-      for (int i = 0; i < KI; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[nr][i][j][e] = 0.f;
     }
+    __syncwarp();
+    return true;
+  };
+  int copied = 0;
+  bool ok = true;
+  if (warp == 0)
+    for (; copied < min(nst, G::STAGES) && ok; ++copied) ok = copy_stage(copied);
 
-    const int all_see = min(ke, kv4_row_limit(p, rq, R0 / p.group));   // every row of the tile sees the keys below
-    const bool rows_full = R0 + G::kRows <= n_rows;
-    const Kv4Masks masks{p.mask_low, p.mask_high};
-    bool ok = true;
-    for (int it = 0; it < nst; ++it) {
-      const int st = it % G::STAGES;
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (it / G::STAGES) & 1, flags))) { ok = false; break; }
-      const int t0 = ks + it * G::KEYS + 16 * warp;
-      if (t0 < ke) {
-        const uint8_t* kc = smem + st * G::kStage + 16 * warp * (HD / 2);
-        const uint8_t* kS = smem + st * G::kStage + G::kCodes + 16 * warp * (HD / 16);
-        const uint8_t* vc = kc + G::kCodes + G::kScales;
-        const uint8_t* vS = kS + G::kCodes + G::kScales;
-        float s[NR][4];
+  const int r = lane >> 2, c = lane & 3;
+  uint32_t qf[NR][KI][8];               // fp16, scaled by a power of two per row
+  int lim[NR][2];                       // columns 2c, 2c + 1: keys the row sees end here
+  float fac[NR][2];                     // and what turns their sums into log2 weights
+  float m[NR][2], l[NR][2];
+  float o[NR][KI][4][4];
+#pragma unroll
+  for (int nr = 0; nr < NR; ++nr) {
+    const int R = R0 + 8 * nr + r;
+    const bool real = R < n_rows;
+    const bf16_t* qr = p.q + (long)(rq.q0 + (real ? R / p.group : 0)) * p.q_tok + (g * p.group + (real ? R % p.group : 0)) * p.q_head;
+#pragma unroll
+    for (int i = 0; i < KI; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int d = 64 * i + 16 * c + 8 * h;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (real && d < HD) v = *reinterpret_cast<const uint4*>(qr + d);
+        qf[nr][i][4 * h] = v.x;
+        qf[nr][i][4 * h + 1] = v.y;
+        qf[nr][i][4 * h + 2] = v.z;
+        qf[nr][i][4 * h + 3] = v.w;
+      }
+    // the row's largest magnitude to [2^14, 2^15): bf16 bits compare like their magnitudes
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < KI; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, max(qf[nr][i][e] & 0x7FFFu, (qf[nr][i][e] >> 16) & 0x7FFFu));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // exponent field e: times 2^(141 - e), in two factors that are normal numbers for every e
+    const int up = 141 - max((int)(top >> 7), 15);          // -114 .. 126
+    const float scale_q = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+    for (int i = 0; i < KI; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const __half2 v = __floats2half2_rn(__uint_as_float(qf[nr][i][e] << 16) * scale_q,
+                                            __uint_as_float(qf[nr][i][e] & 0xFFFF0000u) * scale_q);
+        qf[nr][i][e] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    const float down = __uint_as_float((uint32_t)(127 - up) << 23);   // 2^-up: normal
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int Rc = R0 + 8 * nr + 2 * c + e;
+      lim[nr][e] = Rc < n_rows ? min(ke, kv4_row_limit(p, rq, Rc / p.group)) : 0;
+      fac[nr][e] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + e)) * 16.f * p.scale_log2;
+      m[nr][e] = -INFINITY;
+      l[nr][e] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < KI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nr][i][j][e] = 0.f;
+  }
+
+  const int all_see = min(ke, kv4_row_limit(p, rq, R0 / p.group));   // every row of the tile sees the keys below
+  const bool rows_full = R0 + G::kRows <= n_rows;
+  const Kv4Masks masks{p.mask_low, p.mask_high};
+  for (int it = 0; it < nst && ok; ++it) {
+    const int st = it % G::STAGES;
+    // the stage that was read last is filled again while this one is being read
+    if (warp == 0 && it > 0 && copied < nst) {
+      ok = copy_stage(copied);
+      if (!ok) break;
+      ++copied;
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (it / G::STAGES) & 1, flags))) { ok = false; break; }
+    const int t0 = ks + it * G::KEYS + 16 * TI * warp;
+    if (t0 < ke) {
+      const uint8_t* kc = smem + st * G::kStage + 16 * TI * warp * (HD / 2);
+      const uint8_t* kS = smem + st * G::kStage + G::kCodes + 16 * TI * warp * (HD / 16);
+      const uint8_t* vc = kc + G::kCodes + G::kScales;
+      const uint8_t* vS = kS + G::kCodes + G::kScales;
+      float s[TI][NR][4];
+#pragma unroll
+      for (int u = 0; u < TI; ++u)
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nr][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[u][nr][e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < KI; ++i) {
-          const int grp = 4 * i + c;
-          const bool in = 64 * (i + 1) <= HD || 16 * grp < HD;
+      for (int i = 0; i < KI; ++i) {
+        const int grp = 4 * i + c;
+        const bool in = 64 * (i + 1) <= HD || 16 * grp < HD;
+#pragma unroll
+        for (int u = 0; u < TI; ++u) {
+          const int ra = 16 * u + r, rb = ra + 8;
           uint2 wa = make_uint2(0, 0), wb = wa;
           uint32_t ba = 0, bb = 0;
           if (in) {
-            wa = *reinterpret_cast<const uint2*>(kc + r * (HD / 2) + 8 * grp);
-            wb = *reinterpret_cast<const uint2*>(kc + (r + 8) * (HD / 2) + 8 * grp);
-            ba = kS[r * (HD / 16) + grp];
-            bb = kS[(r + 8) * (HD / 16) + grp];
+            wa = *reinterpret_cast<const uint2*>(kc + ra * (HD / 2) + 8 * grp);
+            wb = *reinterpret_cast<const uint2*>(kc + rb * (HD / 2) + 8 * grp);
+            ba = kS[ra * (HD / 16) + grp];
+            bb = kS[rb * (HD / 16) + grp];
           }
           const Kv4Scale2 sa = kv4_scale2(ba * 0x00800080u), sb = kv4_scale2(bb * 0x00800080u);
 #pragma unroll
@@ -357,61 +367,72 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
               const uint32_t a[4] = {xa[2 * k], xb[2 * k], xa[2 * k + 1], xb[2 * k + 1]};
 #pragma unroll
               for (int nr = 0; nr < NR; ++nr)
-                mma_f16_16816(s[nr], a, qf[nr][i][4 * h + 2 * k], qf[nr][i][4 * h + 2 * k + 1]);
+                mma_f16_16816(s[u][nr], a, qf[nr][i][4 * h + 2 * k], qf[nr][i][4 * h + 2 * k + 1]);
             }
           }
         }
-        uint32_t pf[NR][2];
+      }
+      uint32_t pf[TI][NR][2];
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
+      for (int nr = 0; nr < NR; ++nr) {
+        float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nr][e] *= fac[nr][e & 1];
-          if (t0 + 16 > all_see || !rows_full) {
+        for (int u = 0; u < TI; ++u) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[u][nr][e] *= fac[nr][e & 1];
+          if (t0 + 16 * TI > all_see || !rows_full) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (t0 + r + 8 * (e >> 1) >= lim[nr][e & 1]) s[nr][e] = -INFINITY;
+              if (t0 + 16 * u + r + 8 * (e >> 1) >= lim[nr][e & 1]) s[u][nr][e] = -INFINITY;
           }
-          const float mx0 = fmaxf(s[nr][0], s[nr][2]), mx1 = fmaxf(s[nr][1], s[nr][3]);
-          // a new reference only when a score is more than 2^14 above it (the first visible key always is)
-          if (__any_sync(0xffffffffu, mx0 > m[nr][0] + (kKv4Low + 8.f) || mx1 > m[nr][1] + (kKv4Low + 8.f))) {
-            float f[2];
+          mx0 = fmaxf(mx0, fmaxf(s[u][nr][0], s[u][nr][2]));
+          mx1 = fmaxf(mx1, fmaxf(s[u][nr][1], s[u][nr][3]));
+        }
+        // a new reference only when a score is more than 2^14 above it (the first visible key always is)
+        if (__any_sync(0xffffffffu, mx0 > m[nr][0] + (kKv4Low + 8.f) || mx1 > m[nr][1] + (kKv4Low + 8.f))) {
+          float f[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float mx = e ? mx1 : mx0;
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float mn = fmaxf(m[nr][e], mx - kKv4Low);
-              f[e] = mn == -INFINITY ? 1.f : exp2f(m[nr][e] - mn);
-              m[nr][e] = mn;
-              l[nr][e] *= f[e];
-            }
-#pragma unroll
-            for (int i = 0; i < KI; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[nr][i][j][e] *= f[e & 1];
+          for (int e = 0; e < 2; ++e) {
+            float mx = e ? mx1 : mx0;
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = fmaxf(m[nr][e], mx - kKv4Low);
+            f[e] = mn == -INFINITY ? 1.f : exp2f(m[nr][e] - mn);
+            m[nr][e] = mn;
+            l[nr][e] *= f[e];
           }
-          const float b0 = m[nr][0] == -INFINITY ? 0.f : m[nr][0], b1 = m[nr][1] == -INFINITY ? 0.f : m[nr][1];
-          const float p0 = ex2_approx(s[nr][0] - b0), p1 = ex2_approx(s[nr][1] - b1);
-          const float p2 = ex2_approx(s[nr][2] - b0), p3 = ex2_approx(s[nr][3] - b1);
+#pragma unroll
+          for (int i = 0; i < KI; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nr][i][j][e] *= f[e & 1];
+        }
+        const float b0 = m[nr][0] == -INFINITY ? 0.f : m[nr][0], b1 = m[nr][1] == -INFINITY ? 0.f : m[nr][1];
+#pragma unroll
+        for (int u = 0; u < TI; ++u) {
+          const float p0 = ex2_approx(s[u][nr][0] - b0), p1 = ex2_approx(s[u][nr][1] - b1);
+          const float p2 = ex2_approx(s[u][nr][2] - b0), p3 = ex2_approx(s[u][nr][3] - b1);
           l[nr][0] += p0 + p2;
           l[nr][1] += p1 + p3;
           const __half2 h01 = __floats2half2_rn(p0, p1), h23 = __floats2half2_rn(p2, p3);
-          pf[nr][0] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h01));
-          pf[nr][1] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h23));
+          pf[u][nr][0] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h01));
+          pf[u][nr][1] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h23));
         }
-        const bool tail = t0 + 16 > ke;   // keys past the end: what their bytes hold is not used, not even times 0
+      }
+      const bool tail = t0 + 16 * TI > ke;   // keys past the end: what their bytes hold is not used, not even times 0
 #pragma unroll
-        for (int i = 0; i < KI; ++i) {
-          const int w = 8 * i + r;
-          const bool in = 8 * (i + 1) <= WORDS || w < WORDS;
+      for (int i = 0; i < KI; ++i) {
+        const int w = 8 * i + r;
+        const bool in = 8 * (i + 1) <= WORDS || w < WORDS;
+#pragma unroll
+        for (int u = 0; u < TI; ++u) {
           uint32_t x[4] = {0, 0, 0, 0}, sc[4] = {0, 0, 0, 0};
           if (in) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int t = 2 * c + (e & 1) + 8 * (e >> 1);
+              const int t = 16 * u + 2 * c + (e & 1) + 8 * (e >> 1);
               x[e] = *reinterpret_cast<const uint32_t*>(vc + t * (HD / 2) + 4 * w);
               sc[e] = vS[t * (HD / 16) + w / 2];
             }
@@ -419,7 +440,7 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
           if (tail) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (t0 + 2 * c + (e & 1) + 8 * (e >> 1) >= ke) sc[e] = 0;
+              if (t0 + 16 * u + 2 * c + (e & 1) + 8 * (e >> 1) >= ke) sc[e] = 0;
           }
           const Kv4Scale2 s0 = kv4_scale2((sc[1] * 65536u + sc[0]) * 128u), s1 = kv4_scale2((sc[3] * 65536u + sc[2]) * 128u);
           uint32_t e0[4], d0[4], e1[4], d1[4];   // even and odd dims of the two pairs of tokens
@@ -431,42 +452,45 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
           for (int j = 0; j < 4; ++j) {
             const uint32_t a[4] = {e0[j], d0[j], e1[j], d1[j]};
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr) mma_f16_16816(o[nr][i][j], a, pf[nr][0], pf[nr][1]);
+            for (int nr = 0; nr < NR; ++nr) mma_f16_16816(o[nr][i][j], a, pf[u][nr][0], pf[u][nr][1]);
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
     }
-    if (!ok) flags[0] = 1;
-    __syncthreads();   // every copy has landed and every stage is read: the stages' memory is free
-    // ---------------- each warp's reference, sum and O of its rows
-    float* red = reinterpret_cast<float*>(smem) + warp * G::kRows * (HD + 2);
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float sum = l[nr][e];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        float* row = red + (8 * nr + 2 * c + e) * (HD + 2);
-        if (r == 0) {
-          row[HD] = m[nr][e];
-          row[HD + 1] = sum;
-        }
-#pragma unroll
-        for (int i = 0; i < KI; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (8 * i + r < WORDS)
-              *reinterpret_cast<float2*>(row + 8 * (8 * i + r) + 2 * j) = make_float2(o[nr][i][j][e], o[nr][i][j][2 + e]);
-      }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
   }
+  if (!ok) flags[0] = 1;
+  // whatever became of the waits, the copies already issued land before the stages are used otherwise
+  if (warp == 0)
+    for (int i = max(0, copied - G::STAGES); i < copied; ++i) mbar_drain(&full[i % G::STAGES], (i / G::STAGES) & 1);
+  __syncthreads();   // every copy has landed and every stage is read: the stages' memory is free
+  // ---------------- each warp's reference, sum and O of its rows
+  float* red = reinterpret_cast<float*>(smem) + warp * G::kRows * (HD + 2);
+#pragma unroll
+  for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float sum = l[nr][e];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      float* row = red + (8 * nr + 2 * c + e) * (HD + 2);
+      if (r == 0) {
+        row[HD] = m[nr][e];
+        row[HD + 1] = sum;
+      }
+#pragma unroll
+      for (int i = 0; i < KI; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (8 * i + r < WORDS)
+            *reinterpret_cast<float2*>(row + 8 * (8 * i + r) + 2 * j) = make_float2(o[nr][i][j][e], o[nr][i][j][2 + e]);
+    }
   __syncthreads();
   // ---------------- the warps' results joined
   const bool lost = flags[0] != 0 || flags[1] != 0;
-  const float* red = reinterpret_cast<const float*>(smem);
+  const float* all = reinterpret_cast<const float*>(smem);
   for (int u = threadIdx.x; u < G::kRows * (HD / 2); u += G::THREADS) {
     const int rr = u / (HD / 2), d = 2 * (u - rr * (HD / 2));
     const int R = R0 + rr;
@@ -474,13 +498,13 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
     float mw[G::WARPS], mx = -INFINITY;
 #pragma unroll
     for (int w = 0; w < G::WARPS; ++w) {
-      mw[w] = red[(w * G::kRows + rr) * (HD + 2) + HD];
+      mw[w] = all[(w * G::kRows + rr) * (HD + 2) + HD];
       mx = fmaxf(mx, mw[w]);
     }
     float sum = 0.f, a0 = 0.f, a1 = 0.f;
 #pragma unroll
     for (int w = 0; w < G::WARPS; ++w) {
-      const float* row = red + (w * G::kRows + rr) * (HD + 2);
+      const float* row = all + (w * G::kRows + rr) * (HD + 2);
       if (row[HD + 1] == 0.f) continue;   // no key seen
       // a reference at -inf with a sum: every score was NaN, and so is the sum
       const float f = mw[w] == -INFINITY ? 1.f : exp2f(mw[w] - mx);

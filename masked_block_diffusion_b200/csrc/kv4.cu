@@ -119,20 +119,21 @@ AttnPlan attn_plan(int B, int max_q, int max_kv, int group, int Hkv) {
   a.nr = rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
   a.tiles = ceil_div(rows, a.nr ? 8 * a.nr : 256);
   // Blocks that the GPU holds at a time, and blocks without a split.
-  const long slots = kSMs * (a.nr == 1 ? 3 : a.nr == 2 ? 2 : 1);
+  const long slots = kSMs * (a.nr == 1 ? 4 : a.nr == 2 ? 2 : 1);
   const long blocks = (long)B * Hkv * a.tiles;
   long want;
   if (a.nr == 0) {
     want = slots / blocks;
   } else if (blocks * ceil_div(max_kv, 256) <= slots) {
-    want = ceil_div(max_kv, 64);                       // a short call: as wide as it goes
+    want = ceil_div(max_kv, 128);                      // a short call: as wide as it goes
   } else {
     // one wave of blocks when a few requests share the GPU; else blocks of 512 keys or more and
     // about four waves of them, so that requests of different lengths even out
     want = blocks >= slots / 4 ? std::min<long>(ceil_div(4 * slots, blocks), ceil_div(max_kv, 512)) : slots / blocks;
   }
   want = std::max(1L, std::min<long>(want, ceil_div(max_kv, a.nr ? 64 : 128)));
-  a.chunk = std::max(64, ceil_div(ceil_div(max_kv, want), 64) * 64);
+  const int grain = a.nr ? 128 : 64;   // keys of a kernel's stage
+  a.chunk = std::max(grain, ceil_div(ceil_div(max_kv, want), grain) * grain);
   a.n_splits = std::max(1, ceil_div(max_kv, a.chunk));
   return a;
 }
