@@ -25,7 +25,9 @@ def __getattr__(name):
     # kv4 works on torch tensors; the package itself imports torch only when it is used
     if name in ("KVCache4", "Rope", "rope"):
         from . import kv4
-        return getattr(kv4, name)
+        for n in ("KVCache4", "Rope", "rope"):
+            globals()[n] = getattr(kv4, n)
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

@@ -125,11 +125,11 @@ AttnPlan attn_plan(int B, int max_q, int max_kv, int group, int Hkv) {
   if (a.nr == 0) {
     want = slots / blocks;
   } else if (blocks * ceil_div(max_kv, 256) <= slots) {
-    want = ceil_div(max_kv, 128);                      // a short call: as wide as it goes
+    want = ceil_div(max_kv, 256);                      // a short call: as wide as it goes
   } else {
     // one wave of blocks when a few requests share the GPU; else blocks of 512 keys or more and
-    // about four waves of them, so that requests of different lengths even out
-    want = blocks >= slots / 4 ? std::min<long>(ceil_div(4 * slots, blocks), ceil_div(max_kv, 512)) : slots / blocks;
+    // about two waves of them, so that requests of different lengths even out
+    want = blocks >= slots / 4 ? std::min<long>(ceil_div(2 * slots, blocks), ceil_div(max_kv, 512)) : slots / blocks;
   }
   want = std::max(1L, std::min<long>(want, ceil_div(max_kv, a.nr ? 64 : 128)));
   const int grain = a.nr ? 128 : 64;   // keys of a kernel's stage

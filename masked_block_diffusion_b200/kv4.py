@@ -13,6 +13,7 @@ streams' work on them.
 
 from __future__ import annotations
 
+import contextlib
 from typing import Optional, Tuple
 
 import torch
@@ -92,19 +93,18 @@ def _table(t: torch.Tensor, dev: int) -> tuple:
     return t.data_ptr(), rows, sr if rows > 1 else cols
 
 
-def _no_grad(*tensors) -> None:
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+def _refuse_grad() -> None:
+    if torch.is_grad_enabled():
         raise RuntimeError("these operations record no gradient: call them on detached tensors "
                            "(rope(..., transposed=True) is the gradient of rope)")
 
 
-def _launch(dev: int, op, *args) -> None:
-    """op(*args, stream) with device `dev` current, on its current stream."""
-    if _current_device() == dev:
-        op(*args, _stream_of(dev))
-    else:
-        with torch.cuda.device(dev):
-            op(*args, _stream_of(dev))
+_HERE = contextlib.nullcontext()
+
+
+def _on(dev: int):
+    """Makes device `dev` current for a launch, where it is not."""
+    return _HERE if _current_device() == dev else torch.cuda.device(dev)
 
 
 def _device_of(name: str, t: torch.Tensor) -> int:
@@ -125,18 +125,24 @@ def rope(x: torch.Tensor, pos: torch.Tensor, plan: Rope, out: Optional[torch.Ten
     dev = _device_of("x", x)
     T, H, hd = x.shape
     xt, xh = _heads("x", x, dev, T, H, hd, _TYPES)
-    _no_grad(x, out)
     at = _ints("pos", pos, dev, T)
     if out is None:
         dtype = out_dtype or x.dtype
         if dtype not in _TYPES:
             _bad("out_dtype", f"{dtype}, expected one of {[str(d) for d in _TYPES]}")
-        out = x.new_empty((T, H, hd), dtype=dtype)
-    elif out_dtype is not None and out_dtype != out.dtype:
-        _bad("out", f"{out.dtype}, but out_dtype is {out_dtype}")
-    yt, yh = _heads("out", out, dev, T, H, hd, _TYPES)
-    _launch(dev, binding.dllm_op_rope, plan.c, x.data_ptr(), _TYPES[x.dtype], xt, xh, at, T, H, hd, out.data_ptr(),
-            _TYPES[out.dtype], yt, yh, 1 if transposed else 0)
+        out = torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+        yt, yh = H * hd, hd
+    else:
+        if out_dtype is not None and out_dtype != out.dtype:
+            _bad("out", f"{out.dtype}, but out_dtype is {out_dtype}")
+        if out.requires_grad:
+            _refuse_grad()
+        yt, yh = _heads("out", out, dev, T, H, hd, _TYPES)
+    if x.requires_grad:
+        _refuse_grad()
+    with _on(dev):
+        binding.dllm_op_rope(plan.c, x.data_ptr(), _TYPES[x.dtype], xt, xh, at, T, H, hd, out.data_ptr(),
+                             _TYPES[out.dtype], yt, yh, 1 if transposed else 0, _stream_of(dev))
     return out
 
 
@@ -178,6 +184,7 @@ class KVCache4:
         self.codes, self.scales, self.device = codes, scales, codes.device
         self.n_pages, _, self.n_kv_heads, self.page = codes.shape[:4]
         self.head_dim = 2 * codes.shape[4]
+        self._sizes = {}
         self.c = binding.dllm_kv4(codes.data_ptr(), scales.data_ptr(), self.n_pages, self.page, self.n_kv_heads,
                                   self.head_dim)
         self._dev = _device_of("codes, scales", codes)
@@ -191,11 +198,15 @@ class KVCache4:
         T, H, d, dev = k.shape[0], self.n_kv_heads, self.head_dim, self._dev
         kt, kh = _heads("k", k, dev, T, H, d, _TYPES)
         vt, vh = _heads("v", v, dev, T, H, d, (k.dtype,))
-        _no_grad(k, v)
-        _launch(dev, binding.dllm_op_append_kv4, self.c, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _TYPES[k.dtype],
-                _ints("req", req, dev, T), _ints("pos", pos, dev, T),
-                None if rope_pos is None else _ints("rope_pos", rope_pos, dev, T), T, *_table(table, dev),
-                None if rope is None else rope.c)
+        if k.requires_grad or v.requires_grad:
+            _refuse_grad()
+        req_ptr, pos_ptr = _ints("req", req, dev, T), _ints("pos", pos, dev, T)
+        rope_ptr = None if rope_pos is None else _ints("rope_pos", rope_pos, dev, T)
+        tab, rows, stride = _table(table, dev)
+        with _on(dev):
+            binding.dllm_op_append_kv4(self.c, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _TYPES[k.dtype], req_ptr,
+                                       pos_ptr, rope_ptr, T, tab, rows, stride, None if rope is None else rope.c,
+                                       _stream_of(dev))
 
     def read(self, req: torch.Tensor, pos: torch.Tensor, table: torch.Tensor, k_out: Optional[torch.Tensor] = None,
              v_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -213,8 +224,11 @@ class KVCache4:
                 if not t.is_contiguous():
                     _bad(name, "has to be contiguous")
             outs.append(t)
-        _launch(dev, binding.dllm_op_read_kv4, self.c, _ints("req", req, dev, T), _ints("pos", pos, dev, T), T,
-                *_table(table, dev), outs[0].data_ptr(), outs[1].data_ptr(), 1 if made else 0)
+        req_ptr, pos_ptr = _ints("req", req, dev, T), _ints("pos", pos, dev, T)
+        tab, rows, stride = _table(table, dev)
+        with _on(dev):
+            binding.dllm_op_read_kv4(self.c, req_ptr, pos_ptr, T, tab, rows, stride, outs[0].data_ptr(),
+                                     outs[1].data_ptr(), 1 if made else 0, _stream_of(dev))
         return outs[0], outs[1]
 
     def attend(self, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor, max_q: int,
@@ -232,13 +246,16 @@ class KVCache4:
         T, H, hd = q.shape
         dev, B = self._dev, kv_len.shape[0]
         qt, qh = _heads("q", q, dev, T, H, self.head_dim, (torch.bfloat16,))
-        _no_grad(q)
+        if q.requires_grad:
+            _refuse_grad()
         tab, rows, stride = _table(table, dev)
         if rows < B:
             _bad("table", f"{rows} rows for {B} requests")
         if out is None:
-            out = q.new_empty((T, H, hd))
-        ot, oh = _heads("out", out, dev, T, H, hd, (torch.bfloat16,))
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            ot, oh = H * hd, hd
+        else:
+            ot, oh = _heads("out", out, dev, T, H, hd, (torch.bfloat16,))
         lse = q.new_empty((T, H), dtype=torch.float32) if return_lse else None
         if workspace is None:
             size = self.workspace_bytes(B, T, max_q, max_kv, H)
@@ -248,12 +265,21 @@ class KVCache4:
             if workspace.get_device() != dev or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
                 _bad("workspace", "expected a contiguous uint8 tensor on the cache's device")
             size = workspace.numel()
-        _launch(dev, binding.dllm_op_attn_kv4, self.c, q.data_ptr(), qt, qh, out.data_ptr(), ot, oh,
-                lse.data_ptr() if return_lse else None, _ints("q_start", q_start, dev, B + 1),
-                _ints("kv_len", kv_len, dev, B), B, T, max_q, max_kv, H, tab, stride, 1 if causal else 0,
-                hd ** -0.5 if scale is None else scale, None if workspace is None else workspace.data_ptr(), size)
+        start_ptr, len_ptr = _ints("q_start", q_start, dev, B + 1), _ints("kv_len", kv_len, dev, B)
+        with _on(dev):
+            binding.dllm_op_attn_kv4(self.c, q.data_ptr(), qt, qh, out.data_ptr(), ot, oh,
+                                     lse.data_ptr() if return_lse else None, start_ptr, len_ptr, B, T, max_q, max_kv, H,
+                                     tab, stride, 1 if causal else 0, hd ** -0.5 if scale is None else scale,
+                                     None if workspace is None else workspace.data_ptr(), size, _stream_of(dev))
         return (out, lse) if return_lse else out
 
     def workspace_bytes(self, B: int, T: int, max_q: int, max_kv: int, heads: int) -> int:
         """Bytes of workspace that attend() needs for these sizes."""
-        return binding.dllm_op_attn_kv4_workspace(self.c, B, T, max_q, max_kv, heads)
+        sizes = (B, T, max_q, max_kv, heads)
+        n = self._sizes.get(sizes)
+        if n is None:
+            n = binding.dllm_op_attn_kv4_workspace(self.c, *sizes)
+            if len(self._sizes) >= 1024:
+                self._sizes.clear()
+            self._sizes[sizes] = n
+        return n
