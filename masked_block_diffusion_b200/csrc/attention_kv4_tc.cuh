@@ -9,7 +9,7 @@
 //
 // Roles (640 threads, five warpgroups):
 //   warps 0, 1   each issues one tile's products (warp 0 holds the TMEM allocation): S_t = Q_t K^T
-//                (bf16) into tile t's S columns, and O_t += P_t V (fp16) with P_t read from
+//                into tile t's S columns, and O_t += P_t V, with P_t read from
 //                TMEM. A wait and an issue cost such a warp some 200 cycles each among the busy
 //                warps of its scheduler, so one warp for both tiles was the bottleneck (2450
 //                cycles per 64 keys at head_dim 64). S_t(j + 1) goes out as soon as the
@@ -20,7 +20,7 @@
 //   warps 4..7   softmax of tile 0, warps 8..11 of tile 1: one row per thread (TMEM lane), 64
 //                scores in registers, lazy reference as in attention_kv4.cuh; O is rescaled in
 //                TMEM when the reference moves (rare), and read and written out at the end;
-//   warps 12..19 unpack 8 keys of each block of 64, K to bf16 and V to fp16, both exact, as 64-dim
+//   warps 12..19 unpack 8 keys of each block of 64 to sixteenths in fp16 (exact, attention_kv4.cuh), as 64-dim
 //                atoms of 128-byte rows with the 128-byte swizzle (K's rows are keys, K-major; V's
 //                are the same rows read as the MN-major operand). Eight consecutive lanes write
 //                4 groups of 2 adjacent keys: 8 different 16-byte columns, no bank conflict. The
@@ -38,9 +38,9 @@
 
 namespace dllm {
 
-// Instruction descriptor: fp16 A (K-major) x fp16 B (MN-major), fp32 D.
-__host__ __device__ constexpr uint32_t idesc_f16_f32_bmn(int M, int N) {
-  return (1u << 4) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor: fp16 A and B, both K-major, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // True in one lane of a converged warp, always the same one. The warp that issues the products
@@ -92,7 +92,8 @@ DLLM_DEV void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::
 // Tile t's softmax: thread (warp w, lane) owns row 32 (w % 4) + lane of the tile.
 template <int HD>
 DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_t tmem_base, uint64_t* s_full,
-                               uint64_t* s_read, uint64_t* p_full, uint64_t* pv_done, volatile int* flags,
+                               uint64_t* s_read, uint64_t* p_full, uint64_t* pv_done, uint64_t* q_full,
+                               uint8_t* q_smem, volatile int* flags,
                                int t, int nt, int R0, int g, int sp, int ks, int ke, int nblk) {
   using G = AttnKv4TcCfg<HD>;
   constexpr int BK = G::BK;
@@ -109,6 +110,39 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_
   const int R = R0 + 128 * t + row;
   const bool real = R < rq.n * p.group;
   const int lim = real ? min(ke, kv4_row_limit(p, rq, R / p.group)) : ke;
+  // The thread's row of Q: to fp16, times a power of two that takes its largest magnitude to
+  // [2^14, 2^15) (attention_kv4.cuh), then 16-byte chunk c to column c ^ (row % 8) of its atom's
+  // 128-byte row. Rows past the last are 0.
+  float fac;   // from the sums of products with K's sixteenths to log2 weights
+  {
+    uint4 q[HD / 8];
+    const bf16_t* src = p.q + (long)(rq.q0 + (real ? R / p.group : 0)) * p.q_tok + (g * p.group + (real ? R % p.group : 0)) * p.q_head;
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < HD / 8; ++c) q[c] = real ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int c = 0; c < HD / 8; ++c) {
+      const uint32_t w[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+    }
+    const int up = 141 - max((int)(top >> 7), 15);
+    const float scale_q = __uint_as_float((uint32_t)(127 + up) << 23);
+    fac = __uint_as_float((uint32_t)(127 - up) << 23) * 16.f * p.scale_log2;
+#pragma unroll
+    for (int c = 0; c < HD / 8; ++c) {
+      uint32_t w[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __half2 v = __floats2half2_rn(__uint_as_float(w[e] << 16) * scale_q, __uint_as_float(w[e] & 0xFFFF0000u) * scale_q);
+        w[e] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      *reinterpret_cast<uint4*>(q_smem + (c >> 3) * 128 * 128 + row * 128 + (((c ^ row) & 7) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_full[t]);
+  }
   float m = -INFINITY, l = 0.f;
   bool ok = true;
   for (int j = 0; j < nblk; ++j) {
@@ -125,7 +159,7 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_
       for (int c = 0; c < BK; ++c)
         if (c >= seen) s[c] = -INFINITY;
     }
-    const float mx = tree_max<BK>(s) * p.scale_log2;
+    const float mx = tree_max<BK>(s) * fac;
     if (j == 0) {
       m = mx - kKv4Low;
     } else {
@@ -150,7 +184,7 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_
     }
     const float mb = m == -INFINITY ? 0.f : m;
     uint32_t pk[BK / 2];
-    const uint64_t sc2 = pack_f32x2(p.scale_log2, p.scale_log2), mb2 = pack_f32x2(-mb, -mb);
+    const uint64_t sc2 = pack_f32x2(fac, fac), mb2 = pack_f32x2(-mb, -mb);
     uint64_t sum[4] = {0, 0, 0, 0};   // pairs of fp32 sums
 #pragma unroll
     for (int c = 0; c < BK; c += 2) {
@@ -180,7 +214,7 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_
   tc_fence_after();
   const bool lost = flags[0] != 0 || flags[1] != 0;
   const float nan = __int_as_float(0x7FC00000);
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  const float inv = l == 0.f ? 0.f : 16.0f / l;   // V came in sixteenths
   const float lse2 = lost ? nan : l == 0.f ? -INFINITY : m + log2f(l);
   const long tok = rq.q0 + R / p.group;
   const int h = g * p.group + R % p.group;
@@ -224,8 +258,8 @@ __global__ void __launch_bounds__(AttnKv4TcCfg<HD>::THREADS, 1)
 attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
   using G = AttnKv4TcCfg<HD>;
   constexpr int BK = G::BK, AT = G::ATOMS, KST = G::KST, VST = G::VST;
-  constexpr uint32_t kIdQK = idesc_bf16_f32(128, BK);
-  constexpr uint32_t kIdPV = idesc_f16_f32_bmn(128, HD);
+  constexpr uint32_t kIdQK = idesc_f16_f32(128, BK);
+  constexpr uint32_t kIdPV = idesc_f16_f32(128, HD) | (1u << 16);   // B MN-major
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem + G::kOffK;
@@ -238,7 +272,8 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
   uint64_t* s_read = s_full + 2;     // [2]: the softmax has it in registers
   uint64_t* p_full = s_read + 2;     // [2]: P_t(j) is in its columns
   uint64_t* pv_done = p_full + 2;    // [2]: P_t V(j) completed
-  uint64_t* drain = pv_done + 2;     // [2]
+  uint64_t* q_full = pv_done + 2;    // [2]: tile t's Q is in shared memory
+  uint64_t* drain = q_full + 2;      // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [0] abort, [1] a page that is none
 
@@ -274,6 +309,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
       mbar_init(&s_read[t], 4);
       mbar_init(&p_full[t], 4);
       mbar_init(&pv_done[t], 1);
+      mbar_init(&q_full[t], 4);
       mbar_init(&drain[t], 1);
     }
     flags[0] = flags[1] = 0;
@@ -283,16 +319,6 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     tmem_alloc(tmem_slot, G::kTmemCols);
     tmem_relinquish();
   }
-  // Q: 16-byte chunk c of row r at column c ^ (r % 8) of its atom's 128-byte row; rows past the last are 0
-  for (int u = threadIdx.x; u < nt * 128 * (HD / 8); u += G::THREADS) {
-    const int r = u / (HD / 8), c = u - r * (HD / 8);
-    const int R = R0 + r;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (R < n_rows)
-      v = *reinterpret_cast<const uint4*>(p.q + (long)(rq.q0 + R / p.group) * p.q_tok + (g * p.group + R % p.group) * p.q_head + 8 * c);
-    *reinterpret_cast<uint4*>(smem + (r >> 7) * G::kQTile + (c >> 3) * 128 * 128 + (r & 127) * 128 + (((c ^ r) & 7) << 4)) = v;
-  }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -329,7 +355,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
         if (++kst == KST) { kst = 0; kph ^= 1; }
         return true;
       };
-      bool ok = nblk == 0 || issue_s();
+      bool ok = nblk == 0 || (wait(&q_full[t], 0) && issue_s());
       for (int j = 0; j < nblk && ok; ++j) {
         if (j + 1 < nblk && !(wait(&s_read[t], j & 1) && issue_s())) { ok = false; break; }
         if (!wait(&v_full[vst], vph) || !wait(&p_full[t], j & 1)) { ok = false; break; }
@@ -387,6 +413,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
       }
     };
     const uint32_t at0 = key * 128 + (((2 * grp) ^ k8) << 4);
+    const Kv4Masks masks{p.mask_low, p.mask_high};
     // K runs a block ahead of V, as S runs ahead of P V: the turns are K(0), K(1), V(0), K(2), V(1), ...
     int id_v = page_of(0), id_k = page_of(1);
     fetch(0, 0, id_v);
@@ -423,25 +450,10 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
 #pragma unroll
         for (int a = 0; a < AT; ++a) {
           if (16 * (4 * a + grp) < HD) {
-            const uint2 c = now[kv][a];
+            const Kv4Scale2 sc = kv4_scale2(scale[kv][a] * 0x00800080u);
             uint32_t o[8];
-            if (kv == 0) {
-              const __nv_bfloat162 s = kv4_scale_bf16x2(scale[kv][a]);
-              const __nv_bfloat162 m24 = __hmul2(s, __float2bfloat162_rn(-24.f));
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                o[e] = kv4_bf16x2(c.x, e, s, m24);
-                o[4 + e] = kv4_bf16x2(c.y, e, s, m24);
-              }
-            } else {
-              const __half2 s = kv4_half2((scale[kv][a] << 7) * 0x00010001u);
-              const __half2 m24 = __hmul2(s, __float2half2_rn(-24.f));
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                o[e] = kv4_f16x2(c.x, e, s, m24);
-                o[4 + e] = kv4_f16x2(c.y, e, s, m24);
-              }
-            }
+            kv4_sixteenth(now[kv][a].x, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[0]));
+            kv4_sixteenth(now[kv][a].y, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[4]));
             *reinterpret_cast<uint4*>(dst + a * G::kAtom) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4*>(dst2 + a * G::kAtom) = make_uint4(o[4], o[5], o[6], o[7]);
           }
@@ -456,7 +468,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     regs_inc<G::kRegsSoftmax>();
     const int t = (warp - 4) >> 2;
     if (t < nt)
-      kv4_softmax_tile<HD>(p, rq, tmem_base, s_full, s_read, p_full, pv_done, flags, t, nt, R0, g, sp, ks, ke, nblk);
+      kv4_softmax_tile<HD>(p, rq, tmem_base, s_full, s_read, p_full, pv_done, q_full, smem + t * G::kQTile, flags, t, nt, R0, g, sp, ks, ke, nblk);
   }
   __syncwarp();
   tc_fence_before();
