@@ -3,7 +3,7 @@
 // attention_kv4.cuh.
 //
 // One block takes 256 query rows (two tiles of 128) of one KV head over one split of the
-// keys. Unpacking 64 keys costs about as many issue slots as one tile's softmax, so both
+// keys. Unpacking a block's keys costs about as many issue slots as one tile's softmax, so both
 // tiles read the same unpacked K and V; the two tiles' softmaxes alternate with each other's
 // products on the tensor pipe.
 //
@@ -20,7 +20,7 @@
 //   warps 4..7   softmax of tile 0, warps 8..11 of tile 1: one row per thread (TMEM lane), 64
 //                scores in registers, lazy reference as in attention_kv4.cuh; O is rescaled in
 //                TMEM when the reference moves (rare), and read and written out at the end;
-//   warps 12..19 unpack 8 keys of each block of 64 to sixteenths in fp16 (exact, attention_kv4.cuh), as 64-dim
+//   warps 12..19 unpack 8 (of 128 keys: 16) keys of each block to sixteenths in fp16 (exact, attention_kv4.cuh), as 64-dim
 //                atoms of 128-byte rows with the 128-byte swizzle (K's rows are keys, K-major; V's
 //                are the same rows read as the MN-major operand). Eight consecutive lanes write
 //                4 groups of 2 adjacent keys: 8 different 16-byte columns, no bank conflict. The
@@ -28,9 +28,11 @@
 //                id two blocks ahead.
 // Registers: the launch gives every thread 96; the softmax warpgroups take 136 and leave 72 to the
 // unpacking ones and 64 to the first (2 x 136 + 2 x 72 + 64 = 5 x 96).
-// TMEM: S_t at 64 t, then P, then O_t. At head_dim 176 there is room for one P (32 columns) beside
-// 2 x 64 columns of S and 2 x 176 of O: the tiles use it in turn, each writing once the other's
-// product has read it. Smaller heads have a P for each tile.
+// TMEM: S_0, S_1 (BK columns each), P_0, P_1 (BK / 2), O_0, O_1 (head_dim). Keys per block: as many as fit,
+// which is 128 at head_dim 64, 64 at 128 and 48 at 176: each block costs every role a few waits of 150 to
+// 200 cycles, whatever its size. (At 176 with 64 keys there is room for one P; the tiles took turns at
+// it, and that chain of writing, product and writing again set the pace whatever else was taken out:
+// 16 canvases 183 us.)
 // Every wait is bounded, as in gemm_tc.cuh; a block that gives one up writes NaN.
 #pragma once
 
@@ -60,7 +62,8 @@ DLLM_DEV bool elect_one() {
 
 template <int HD>
 struct AttnKv4TcCfg {
-  static constexpr int BK = 64;
+  static constexpr int BK = HD == 64 ? 128 : HD == 128 ? 64 : 48;   // keys of a block
+  static constexpr int CH = BK < 64 ? BK : 64;           // of which the softmax has this many in registers at a time
   static constexpr int ATOMS = (HD + 63) / 64;
   static constexpr int KST = 3, VST = 2;                 // unpacked stages of K and of V
   static constexpr int kQTile = ATOMS * 128 * 128;
@@ -70,12 +73,12 @@ struct AttnKv4TcCfg {
   static constexpr int kOffV = kOffK + KST * kKV;
   static constexpr int kOffBar = kOffV + VST * kKV;
   static constexpr int kTotal = kOffBar + 256 + 1024;
-  static constexpr bool kOneP = 2 * BK + 2 * (BK / 2) + 2 * HD > 512;
   static constexpr int kPCol = 2 * BK;
-  static constexpr int kOCol = kPCol + (kOneP ? 1 : 2) * (BK / 2);
+  static constexpr int kOCol = 3 * BK;
   static constexpr int kTmemCols = 512;
-  static constexpr int UNPACK = BK / 8;                  // unpacking warps
-  static constexpr int THREADS = 32 * (4 + 8 + UNPACK);
+  static constexpr int GPW = BK > 64 ? BK / 64 : 1;      // groups of 8 keys per unpacking warp
+  static constexpr int UNPACK = BK / 8 / GPW;            // unpacking warps with work
+  static constexpr int THREADS = 32 * (4 + 8 + 8);
   static constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsUnpack = 72, kRegsIssue = 64;
   static_assert(THREADS == 640 && 2 * kRegsSoftmax + 2 * kRegsUnpack + kRegsIssue <= 5 * kRegsLaunch, "register shares");
   static_assert(kOCol + 2 * HD <= kTmemCols, "TMEM");
@@ -89,6 +92,34 @@ DLLM_DEV void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::
 template <int N>
 DLLM_DEV void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
+DLLM_DEV void tmem_st8_nowait(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// N columns of scores into registers, and N / 2 columns of weights out of them (not waited for).
+template <int N>
+DLLM_DEV void kv4_load_scores(uint32_t taddr, float (&s)[N]) {
+  if constexpr (N == 64) {
+    tmem_ld64(taddr, s);
+  } else {
+    static_assert(N == 48);
+    tmem_ld32(taddr, reinterpret_cast<float(&)[32]>(s[0]));
+    tmem_ld16(taddr + 32, reinterpret_cast<float(&)[16]>(s[32]));
+  }
+}
+template <int N>
+DLLM_DEV void kv4_store_weights(uint32_t taddr, const uint32_t (&w)[N / 2]) {
+  if constexpr (N == 64) {
+    tmem_st32_nowait(taddr, w);
+  } else {
+    static_assert(N == 48);
+    tmem_st16_nowait(taddr, reinterpret_cast<const uint32_t(&)[16]>(w[0]));
+    tmem_st8_nowait(taddr + 16, w + 16);
+  }
+}
+
 // Tile t's softmax: thread (warp w, lane) owns row 32 (w % 4) + lane of the tile.
 template <int HD>
 DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_t tmem_base, uint64_t* s_full,
@@ -96,17 +127,13 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_
                                uint8_t* q_smem, volatile int* flags,
                                int t, int nt, int R0, int g, int sp, int ks, int ke, int nblk) {
   using G = AttnKv4TcCfg<HD>;
-  constexpr int BK = G::BK;
+  constexpr int BK = G::BK, CH = G::CH, NCH = BK / CH;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = 32 * (warp & 3) + lane;
   const uint32_t lane_base = tmem_base + ((uint32_t)(32 * (warp & 3)) << 16);
   const uint32_t s_col = lane_base + t * BK;
-  const uint32_t p_col = lane_base + G::kPCol + (G::kOneP ? 0 : t * (BK / 2));
+  const uint32_t p_col = lane_base + G::kPCol + t * (BK / 2);
   const uint32_t o_col = lane_base + G::kOCol + t * HD;
-  // P's columns are free once the last product that read them is done: this tile's of the block before, or
-  // where the tiles share them the other tile's last one (which is later than this tile's)
-  const int before = G::kOneP && nt == 2 ? t ^ 1 : t;
-  const int lag = before < t ? 0 : 1;
   const int R = R0 + 128 * t + row;
   const bool real = R < rq.n * p.group;
   const int lim = real ? min(ke, kv4_row_limit(p, rq, R / p.group)) : ke;
@@ -148,18 +175,24 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_
   for (int j = 0; j < nblk; ++j) {
     if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], j & 1, flags))) { ok = false; break; }
     tc_fence_after();
-    float s[BK];
-    tmem_ld64(s_col, s);
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s_read[t]);
+    float s[CH];
     const int seen = lim - (ks + j * BK);
-    if (seen < BK) {
+    auto load = [&](int q) {
+      kv4_load_scores<CH>(s_col + q * CH, s);
+      if (seen < (q + 1) * CH) {
 #pragma unroll
-      for (int c = 0; c < BK; ++c)
-        if (c >= seen) s[c] = -INFINITY;
+        for (int c = 0; c < CH; ++c)
+          if (q * CH + c >= seen) s[c] = -INFINITY;
+      }
+    };
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int q = 0; q < NCH; ++q) {
+      load(q);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) top[c & 3] = fmaxf(top[c & 3], s[c]);
     }
-    const float mx = tree_max<BK>(s) * fac;
+    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fac;
     if (j == 0) {
       m = mx - kKv4Low;
     } else {
@@ -183,24 +216,34 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_
       }
     }
     const float mb = m == -INFINITY ? 0.f : m;
-    uint32_t pk[BK / 2];
     const uint64_t sc2 = pack_f32x2(fac, fac), mb2 = pack_f32x2(-mb, -mb);
     uint64_t sum[4] = {0, 0, 0, 0};   // pairs of fp32 sums
 #pragma unroll
-    for (int c = 0; c < BK; c += 2) {
-      float a, b;
-      unpack_f32x2(fma_f32x2(pack_f32x2(s[c], s[c + 1]), sc2, mb2), a, b);
-      a = ex2_approx(a);
-      b = ex2_approx(b);
-      sum[(c / 2) & 3] = add_f32x2(sum[(c / 2) & 3], pack_f32x2(a, b));
-      const __half2 h = __floats2half2_rn(a, b);
-      pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int q = NCH - 1; q >= 0; --q) {   // the last chunk is still in registers
+      if (q < NCH - 1) load(q);
+      if (q == 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_read[t]);
+      }
+      uint32_t pk[CH / 2];
+#pragma unroll
+      for (int c = 0; c < CH; c += 2) {
+        float a, b;
+        unpack_f32x2(fma_f32x2(pack_f32x2(s[c], s[c + 1]), sc2, mb2), a, b);
+        a = ex2_approx(a);
+        b = ex2_approx(b);
+        sum[(c / 2) & 3] = add_f32x2(sum[(c / 2) & 3], pack_f32x2(a, b));
+        const __half2 h = __floats2half2_rn(a, b);
+        pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      if (q == NCH - 1 && j > 0) {   // P's columns are free once the product of the block before is done
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[t], (j - 1) & 1, flags))) { ok = false; break; }
+        tc_fence_after();
+      }
+      kv4_store_weights<CH>(p_col + q * (CH / 2), pk);
     }
-    if (j >= lag) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[before], (j - lag) & 1, flags))) { ok = false; break; }
-      tc_fence_after();
-    }
-    tmem_st32_nowait(p_col, pk);
+    if (!ok) break;
     float l0, l1;
     unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), l0, l1);
     l += l0 + l1;
@@ -331,7 +374,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
       // ---------------- MMA issuer of tile `warp`: the warp waits as one, an elected lane issues
       const int t = __shfl_sync(0xffffffffu, warp, 0);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
-      const uint32_t s_col = tm + t * BK, p_col = tm + G::kPCol + (G::kOneP ? 0 : t * (BK / 2)), o_col = tm + G::kOCol + t * HD;
+      const uint32_t s_col = tm + t * BK, p_col = tm + G::kPCol + t * (BK / 2), o_col = tm + G::kOCol + t * HD;
       const uint64_t qd = sdesc_k_sw128(smem_u32(smem + t * G::kQTile));
       const uint64_t kd0 = sdesc_k_sw128(smem_u32(sK)), vd0 = sdesc_mn_sw128(smem_u32(sV), G::kAtom);
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -379,63 +422,79 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     }
   } else if (warp >= 12) {
     regs_dec<G::kRegsUnpack>();
-    // ---------------- unpacking: the warp's 8 keys of each block, lane / 4 the key, lane % 4 the group of an atom
+    // ---------------- unpacking: GPW times 8 keys of each block, lane / 4 the key, lane % 4 the group of an atom
+    constexpr int GPW = G::GPW;
     const int k8 = lane >> 2, grp = lane & 3;
-    const int key = 8 * (warp - 12) + k8;
+    const int key0 = 8 * (warp - 12) + k8;                      // and key0 + 64
     const int* trow = p.table + (long)b * p.stride;
     const int mask = (1 << p.c.page_shift) - 1;
-    // page id of the key in block j; -1 past the end, and for an id that is no page
-    auto page_of = [&](int j) -> int {
-      const int t = ks + j * BK + key;
-      if (j >= nblk || t >= ke) return -1;
-      const int id = trow[t >> p.c.page_shift];
-      if (id >= 0 && id < p.c.n_pages) return id;
-      flags[1] = 1;
-      return -1;
-    };
     const long v_rows = (long)p.c.Hkv << p.c.page_shift, page_rows = 2 * v_rows;
     const int head_row = g << p.c.page_shift;
-    uint2 code[2][AT];
-    uint32_t byte[2][AT];
-    // a block's bytes of K or V; a key that does not exist has scale 0 and becomes 0
-    auto fetch = [&](int kv, int j, int id) {
-      const long r = max(id, 0) * page_rows + (head_row + ((ks + j * BK + key) & mask)) + (kv ? v_rows : 0);
-      const uint8_t* pc = p.c.codes + r * (HD / 2) + 8 * grp;
-      const uint8_t* ps = p.c.scales + r * (HD / 16) + grp;
+    uint2 code[2][GPW][AT];
+    uint32_t byte[2][GPW][AT];
+    int id_k[GPW], id_v[GPW];
+    // page id of a key in block j; -1 past the end, and for an id that is no page
+    auto pages = [&](int j, int (&id)[GPW]) {
 #pragma unroll
-      for (int a = 0; a < AT; ++a) {
-        code[kv][a] = make_uint2(0, 0);
-        byte[kv][a] = 0;
-        if (id >= 0 && 16 * (4 * a + grp) < HD) {
-          code[kv][a] = *reinterpret_cast<const uint2*>(pc + 32 * a);
-          byte[kv][a] = ps[4 * a];
+      for (int i = 0; i < GPW; ++i) {
+        const int t = ks + j * BK + key0 + 64 * i;
+        id[i] = -1;
+        if (j < nblk && t < ke) {
+          const int found = trow[t >> p.c.page_shift];
+          if (found >= 0 && found < p.c.n_pages) id[i] = found;
+          else flags[1] = 1;
         }
       }
     };
-    const uint32_t at0 = key * 128 + (((2 * grp) ^ k8) << 4);
+    // a block's bytes of K or V; a key that does not exist has scale 0 and becomes 0
+    auto fetch = [&](int kv, int j, const int (&id)[GPW]) {
+#pragma unroll
+      for (int i = 0; i < GPW; ++i) {
+        const long r = max(id[i], 0) * page_rows + (head_row + ((ks + j * BK + key0 + 64 * i) & mask)) + (kv ? v_rows : 0);
+        const uint8_t* pc = p.c.codes + r * (HD / 2) + 8 * grp;
+        const uint8_t* ps = p.c.scales + r * (HD / 16) + grp;
+#pragma unroll
+        for (int a = 0; a < AT; ++a) {
+          code[kv][i][a] = make_uint2(0, 0);
+          byte[kv][i][a] = 0;
+          if (id[i] >= 0 && 16 * (4 * a + grp) < HD) {
+            code[kv][i][a] = *reinterpret_cast<const uint2*>(pc + 32 * a);
+            byte[kv][i][a] = ps[4 * a];
+          }
+        }
+      }
+    };
+    const uint32_t at0 = key0 * 128 + (((2 * grp) ^ k8) << 4);
     const Kv4Masks masks{p.mask_low, p.mask_high};
+    bool ok = warp - 12 < G::UNPACK;
+    const bool works = ok;
     // K runs a block ahead of V, as S runs ahead of P V: the turns are K(0), K(1), V(0), K(2), V(1), ...
-    int id_v = page_of(0), id_k = page_of(1);
-    fetch(0, 0, id_v);
-    bool ok = true;
+    if (works) {
+      pages(0, id_v);
+      pages(1, id_k);
+      fetch(0, 0, id_v);
+    }
     for (int j = -1; j < nblk && ok; ++j) {
       // this turn's bytes have had a block's time to arrive; all loads of the next one are issued
       // together before any is waited for again
-      uint2 now[2][AT];
-      uint32_t scale[2][AT];
+      uint2 now[2][GPW][AT];
+      uint32_t scale[2][GPW][AT];
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
-        for (int a = 0; a < AT; ++a) {
-          if (kv == 1 && j < 0) continue;
-          now[kv][a] = code[kv][a];
-          scale[kv][a] = byte[kv][a];
-          asm volatile("" : "+r"(now[kv][a].x), "+r"(now[kv][a].y), "+r"(scale[kv][a]));
-        }
+        for (int i = 0; i < GPW; ++i)
+#pragma unroll
+          for (int a = 0; a < AT; ++a) {
+            if (kv == 1 && j < 0) continue;
+            now[kv][i][a] = code[kv][i][a];
+            scale[kv][i][a] = byte[kv][i][a];
+            asm volatile("" : "+r"(now[kv][i][a].x), "+r"(now[kv][i][a].y), "+r"(scale[kv][i][a]));
+          }
       fetch(0, j + 2, id_k);
       fetch(1, j + 1, id_v);
-      id_v = id_k;
-      id_k = page_of(j + 3);
+#pragma unroll
+      for (int i = 0; i < GPW; ++i) id_v[i] = id_k[i];
+      pages(j + 3, id_k);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const int jb = kv ? j : j + 1;
@@ -448,22 +507,24 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
         uint8_t* dst = (kv ? sV : sK) + st * G::kKV + at0;
         uint8_t* dst2 = (kv ? sV : sK) + st * G::kKV + (at0 ^ 16);
 #pragma unroll
-        for (int a = 0; a < AT; ++a) {
-          if (16 * (4 * a + grp) < HD) {
-            const Kv4Scale2 sc = kv4_scale2(scale[kv][a] * 0x00800080u);
-            uint32_t o[8];
-            kv4_sixteenth(now[kv][a].x, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[0]));
-            kv4_sixteenth(now[kv][a].y, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[4]));
-            *reinterpret_cast<uint4*>(dst + a * G::kAtom) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst2 + a * G::kAtom) = make_uint4(o[4], o[5], o[6], o[7]);
+        for (int i = 0; i < GPW; ++i)
+#pragma unroll
+          for (int a = 0; a < AT; ++a) {
+            if (16 * (4 * a + grp) < HD) {
+              const Kv4Scale2 sc = kv4_scale2(scale[kv][i][a] * 0x00800080u);
+              uint32_t o[8];
+              kv4_sixteenth(now[kv][i][a].x, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[0]));
+              kv4_sixteenth(now[kv][i][a].y, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[4]));
+              *reinterpret_cast<uint4*>(dst + a * G::kAtom + i * 64 * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(dst2 + a * G::kAtom + i * 64 * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
           }
-        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&(kv ? v_full : k_full)[st]);
       }
     }
-    if (!ok) flags[0] = 1;
+    if (works && !ok) flags[0] = 1;
   } else {
     regs_inc<G::kRegsSoftmax>();
     const int t = (warp - 4) >> 2;

@@ -113,7 +113,7 @@ struct AttnPlan {
 };
 
 // Query rows per block: 8 or 16 of the few-row kernel, else 256 of the tensor-core kernel.
-AttnPlan attn_plan(int B, int max_q, int max_kv, int group, int Hkv) {
+AttnPlan attn_plan(int B, int max_q, int max_kv, int group, int Hkv, int hd) {
   AttnPlan a;
   const long rows = (long)max_q * group;
   a.nr = rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
@@ -132,7 +132,7 @@ AttnPlan attn_plan(int B, int max_q, int max_kv, int group, int Hkv) {
     want = blocks >= slots / 4 ? std::min<long>(ceil_div(2 * slots, blocks), ceil_div(max_kv, 512)) : slots / blocks;
   }
   want = std::max(1L, std::min<long>(want, ceil_div(max_kv, a.nr ? 64 : 128)));
-  const int grain = a.nr ? 128 : 64;   // keys of a kernel's stage
+  const int grain = a.nr ? 128 : hd == 64 ? 128 : hd == 128 ? 64 : 48;   // keys of a kernel's stage or block
   a.chunk = std::max(grain, ceil_div(ceil_div(max_kv, want), grain) * grain);
   a.n_splits = std::max(1, ceil_div(max_kv, a.chunk));
   return a;
@@ -305,7 +305,7 @@ int dllm_op_read_kv4(const dllm_kv4* cache, const int32_t* req, const int32_t* p
 long long dllm_op_attn_kv4_workspace(const dllm_kv4* cache, int B, int T, int max_q, int max_kv, int H) {
   if (!cache_ok(cache) || !attn_sizes_ok(cache, B, T, max_q, max_kv, H)) return DLLM_E_INVAL;
   if (B == 0 || max_q == 0) return 0;
-  const AttnPlan a = attn_plan(B, max_q, max_kv, H / cache->n_kv_heads, cache->n_kv_heads);
+  const AttnPlan a = attn_plan(B, max_q, max_kv, H / cache->n_kv_heads, cache->n_kv_heads, cache->head_dim);
   return (long long)attn_workspace(a, T, H, cache->head_dim);
 }
 
@@ -322,7 +322,7 @@ int dllm_op_attn_kv4(const dllm_kv4* cache, const uint16_t* q, long long q_token
       !vectors(out, DLLM_BF16, out_token_stride, out_head_stride) || !aligned16(workspace))
     return DLLM_E_INVAL;
   const int group = H / cache->n_kv_heads;
-  const AttnPlan a = attn_plan(B, max_q, max_kv, group, cache->n_kv_heads);
+  const AttnPlan a = attn_plan(B, max_q, max_kv, group, cache->n_kv_heads, cache->head_dim);
   if ((a.nr ? (long)cache->n_kv_heads * a.tiles : (long)cache->n_kv_heads * B) > 65535 || a.n_splits > 65535)
     return DLLM_E_INVAL;
   if (attn_workspace(a, T, H, cache->head_dim) > (workspace ? workspace_bytes : 0)) return DLLM_E_INVAL;
