@@ -51,6 +51,7 @@ struct AttnKv4Params {
   float* part_o;            // [n_splits][T][H][hd]
   float* part_lse;          // [n_splits][T][H], log2 domain
   uint32_t mask_low, mask_high;   // Kv4Masks
+  uint32_t mask_bf16;             // 0x00780078
 };
 
 // A request's queries and keys. bad: its row range holds, but not its lengths: every row becomes NaN.
@@ -108,14 +109,6 @@ DLLM_DEV uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
-}
-
-// Two fp16 values of nibble pair j: 16 + u in fp16 (u at mantissa bits 6..9), then (16 + u) s - 24 s, exact.
-DLLM_DEV uint32_t kv4_f16x2(uint32_t w, int j, __half2 s, __half2 ms24) {
-  const uint32_t sh = j == 0 ? w << 6 : j == 1 ? w << 2 : w >> (4 * j - 6);
-  const uint32_t u = (sh & 0x03C003C0u) | 0x4C004C00u;
-  const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&u), s, ms24);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 DLLM_DEV __half2 kv4_half2(uint32_t bits) { return *reinterpret_cast<const __half2*>(&bits); }
@@ -255,7 +248,7 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
   int copied = 0;
   bool ok = true;
   if (warp == 0)
-    for (; copied < min(nst, G::STAGES) && ok; ++copied) ok = copy_stage(copied);
+    while (copied < min(nst, G::STAGES) && (ok = copy_stage(copied))) ++copied;
 
   const int r = lane >> 2, c = lane & 3;
   uint32_t qf[NR][KI][8];               // fp16, scaled by a power of two per row
@@ -596,6 +589,58 @@ attn_kv4_merge_kernel(const __grid_constant__ AttnKv4Params p) {
   }
   if (threadIdx.x == 0 && p.lse != nullptr)
     p.lse[t * p.H + h] = nan ? qnan : mx == -INFINITY ? -INFINITY : (mx + log2f(all)) * 0.6931471805599453f;
+}
+
+// The same for up to 32 splits of many rows: one warp per query and head, which has all of a few splits'
+// loads in flight; eight rows a block. Grid (ceil(max_q * H / 8), B).
+template <int HD>
+__global__ void __launch_bounds__(256)
+attn_kv4_merge_rows_kernel(const __grid_constant__ AttnKv4Params p) {
+  constexpr int VI = (HD + 127) / 128;
+  pdl_begin();
+  const int u = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int i = u / p.H, h = u - i * p.H;
+  const Kv4Req rq = kv4_request(p, blockIdx.y);
+  if (rq.skip || rq.bad || i >= rq.n) return;
+  const long at = (long)(rq.q0 + i) * p.H + h;
+  const long row = (long)p.T * p.H;
+  const float lse = lane < p.n_splits ? p.part_lse[lane * row + at] : -INFINITY;
+  float mx = lse;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const bool nan = __any_sync(0xffffffffu, lse != lse);
+  const float w = exp2f(lse - (mx == -INFINITY ? 0.f : mx));
+  const float all = warp_sum(w);
+  float4 acc[VI];
+#pragma unroll
+  for (int v = 0; v < VI; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* po = p.part_o + at * HD + 4 * lane;
+#pragma unroll 4
+  for (int s = 0; s < p.n_splits; ++s) {
+    const float ws = __shfl_sync(0xffffffffu, w, s);
+#pragma unroll
+    for (int v = 0; v < VI; ++v) {
+      if (128 * v + 4 * lane < HD) {
+        const float4 x = *reinterpret_cast<const float4*>(po + s * row * HD + 128 * v);
+        acc[v].x += ws * x.x;
+        acc[v].y += ws * x.y;
+        acc[v].z += ws * x.z;
+        acc[v].w += ws * x.w;
+      }
+    }
+  }
+  const float inv = nan ? __int_as_float(0x7FC00000) : mx == -INFINITY ? 0.f : 1.f / all;
+#pragma unroll
+  for (int v = 0; v < VI; ++v) {
+    const int d = 128 * v + 4 * lane;
+    if (d < HD) {
+      const uint32_t a = (uint32_t)f32_to_bf16_any(acc[v].x * inv) | ((uint32_t)f32_to_bf16_any(acc[v].y * inv) << 16);
+      const uint32_t b = (uint32_t)f32_to_bf16_any(acc[v].z * inv) | ((uint32_t)f32_to_bf16_any(acc[v].w * inv) << 16);
+      *reinterpret_cast<uint2*>(p.out + (rq.q0 + i) * p.o_tok + h * p.o_head + d) = make_uint2(a, b);
+    }
+  }
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[at] = nan ? __int_as_float(0x7FC00000) : mx == -INFINITY ? -INFINITY : (mx + log2f(all)) * 0.6931471805599453f;
 }
 
 }  // namespace dllm

@@ -3,36 +3,31 @@
 // attention_kv4.cuh.
 //
 // One block takes 256 query rows (two tiles of 128) of one KV head over one split of the
-// keys. Unpacking a block's keys costs about as many issue slots as one tile's softmax, so both
-// tiles read the same unpacked K and V; the two tiles' softmaxes alternate with each other's
-// products on the tensor pipe.
+// keys. Both tiles read the same unpacked K and V, which halves the unpacking, and while one
+// tile's softmax turns its scores into weights the tensor pipe runs the other's products.
 //
-// Roles (640 threads, five warpgroups):
+// Roles (512 threads):
 //   warps 0, 1   each issues one tile's products (warp 0 holds the TMEM allocation): S_t = Q_t K^T
-//                into tile t's S columns, and O_t += P_t V, with P_t read from
-//                TMEM. A wait and an issue cost such a warp some 200 cycles each among the busy
-//                warps of its scheduler, so one warp for both tiles was the bottleneck (2450
-//                cycles per 64 keys at head_dim 64). S_t(j + 1) goes out as soon as the
-//                softmax has read S_t(j) into registers, so a tile's next scores are ready when
-//                its softmax is (with P_t written over S_t instead, S_t(j + 1) has to wait for
-//                P_t V(j), and each tile's chain of product, softmax and product bounded the
-//                kernel: 251 us for 16 canvases);
-//   warps 4..7   softmax of tile 0, warps 8..11 of tile 1: one row per thread (TMEM lane), 64
+//                (bf16) into tile t's S columns, and O_t += P_t V (fp16) with P_t read from
+//                TMEM. A wait and an issue cost such a warp 150 to 200 cycles each among the
+//                busy warps of its scheduler, so one warp for both tiles was the bottleneck.
+//                S_t(j + 1) goes out as soon as the softmax has read S_t(j), so a tile's next
+//                scores are ready when its softmax is.
+//   warps 2..5   softmax of tile 0, warps 6..9 of tile 1: one row per thread (TMEM lane), 48
 //                scores in registers, lazy reference as in attention_kv4.cuh; O is rescaled in
-//                TMEM when the reference moves (rare), and read and written out at the end;
-//   warps 12..19 unpack 8 (of 128 keys: 16) keys of each block to sixteenths in fp16 (exact, attention_kv4.cuh), as 64-dim
-//                atoms of 128-byte rows with the 128-byte swizzle (K's rows are keys, K-major; V's
-//                are the same rows read as the MN-major operand). Eight consecutive lanes write
-//                4 groups of 2 adjacent keys: 8 different 16-byte columns, no bank conflict. The
-//                packed bytes come straight into registers, a block of keys ahead, and the page
-//                id two blocks ahead.
-// Registers: the launch gives every thread 96; the softmax warpgroups take 136 and leave 72 to the
-// unpacking ones and 64 to the first (2 x 136 + 2 x 72 + 64 = 5 x 96).
-// TMEM: S_0, S_1 (BK columns each), P_0, P_1 (BK / 2), O_0, O_1 (head_dim). Keys per block: as many as fit,
-// which is 128 at head_dim 64, 64 at 128 and 48 at 176: each block costs every role a few waits of 150 to
-// 200 cycles, whatever its size. (At 176 with 64 keys there is room for one P; the tiles took turns at
-// it, and that chain of writing, product and writing again set the pace whatever else was taken out:
-// 16 canvases 183 us.)
+//                TMEM when the reference moves (rare). They load their rows of Q first, and
+//                write O out through the same shared memory in the end, both along the rows.
+//   warps 10..15 unpack 8 (of 96 keys: 16) keys of each block, K to bf16 and V to sixteenths in
+//                fp16 (both exact), as 64-dim atoms of 128-byte rows with the 128-byte swizzle
+//                (K's rows are keys, K-major; V's are the same rows read as the MN-major operand).
+//                Eight consecutive lanes write 4 groups of 2 adjacent keys: 8 different 16-byte
+//                columns, no bank conflict. The packed bytes come straight into registers, a block
+//                of keys ahead, and the page ids two blocks ahead.
+// TMEM: S_0, S_1 (BK columns each), P_0, P_1 (BK / 2), O_0, O_1 (head_dim). Keys per block: what
+// fits, in multiples of 48, so that six warps unpack: 96 at head_dim 64, else 48.
+// The code has to stay within the instruction cache: three roles run different loops at a time, and
+// with the unrolled forms of loading Q and writing O (150 KB of code in all) every loop ran a
+// quarter slower. What runs once per block is therefore not unrolled.
 // Every wait is bounded, as in gemm_tc.cuh; a block that gives one up writes NaN.
 #pragma once
 
@@ -62,8 +57,8 @@ DLLM_DEV bool elect_one() {
 
 template <int HD>
 struct AttnKv4TcCfg {
-  static constexpr int BK = HD == 64 ? 128 : HD == 128 ? 64 : 48;   // keys of a block
-  static constexpr int CH = BK < 64 ? BK : 64;           // of which the softmax has this many in registers at a time
+  static constexpr int BK = HD == 64 ? 96 : 48;          // keys of a block
+  static constexpr int CH = 48;                          // of which the softmax has this many in registers at a time
   static constexpr int ATOMS = (HD + 63) / 64;
   static constexpr int KST = 3, VST = 2;                 // unpacked stages of K and of V
   static constexpr int kQTile = ATOMS * 128 * 128;
@@ -76,21 +71,13 @@ struct AttnKv4TcCfg {
   static constexpr int kPCol = 2 * BK;
   static constexpr int kOCol = 3 * BK;
   static constexpr int kTmemCols = 512;
-  static constexpr int GPW = BK > 64 ? BK / 64 : 1;      // groups of 8 keys per unpacking warp
-  static constexpr int UNPACK = BK / 8 / GPW;            // unpacking warps with work
-  static constexpr int THREADS = 32 * (4 + 8 + 8);
-  static constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsUnpack = 72, kRegsIssue = 64;
-  static_assert(THREADS == 640 && 2 * kRegsSoftmax + 2 * kRegsUnpack + kRegsIssue <= 5 * kRegsLaunch, "register shares");
+  static constexpr int UNPACK = 6;                       // unpacking warps
+  static constexpr int GPW = BK / 8 / UNPACK;            // groups of 8 keys of a block that each takes
+  static constexpr int THREADS = 32 * (2 + 8 + UNPACK);
   static_assert(kOCol + 2 * HD <= kTmemCols, "TMEM");
   static_assert(kTotal <= 232448, "shared memory");
   static_assert(kOffBar % 16 == 0, "barriers");
 };
-
-// Gives registers back or takes some of those given back, for the executing warpgroup.
-template <int N>
-DLLM_DEV void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-DLLM_DEV void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
 DLLM_DEV void tmem_st8_nowait(uint32_t taddr, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
@@ -98,87 +85,79 @@ DLLM_DEV void tmem_st8_nowait(uint32_t taddr, const uint32_t* v) {
                : "memory");
 }
 
-// N columns of scores into registers, and N / 2 columns of weights out of them (not waited for).
-template <int N>
-DLLM_DEV void kv4_load_scores(uint32_t taddr, float (&s)[N]) {
-  if constexpr (N == 64) {
-    tmem_ld64(taddr, s);
-  } else {
-    static_assert(N == 48);
-    tmem_ld32(taddr, reinterpret_cast<float(&)[32]>(s[0]));
-    tmem_ld16(taddr + 32, reinterpret_cast<float(&)[16]>(s[32]));
-  }
+// 48 columns of scores into registers, and 24 columns of weights out of them (not waited for).
+DLLM_DEV void kv4_load_scores(uint32_t taddr, float (&s)[48]) {
+  tmem_ld32(taddr, reinterpret_cast<float(&)[32]>(s[0]));
+  tmem_ld16(taddr + 32, reinterpret_cast<float(&)[16]>(s[32]));
 }
-template <int N>
-DLLM_DEV void kv4_store_weights(uint32_t taddr, const uint32_t (&w)[N / 2]) {
-  if constexpr (N == 64) {
-    tmem_st32_nowait(taddr, w);
-  } else {
-    static_assert(N == 48);
-    tmem_st16_nowait(taddr, reinterpret_cast<const uint32_t(&)[16]>(w[0]));
-    tmem_st8_nowait(taddr + 16, w + 16);
-  }
+DLLM_DEV void kv4_store_weights(uint32_t taddr, const uint32_t (&w)[24]) {
+  tmem_st16_nowait(taddr, reinterpret_cast<const uint32_t(&)[16]>(w[0]));
+  tmem_st8_nowait(taddr + 16, w + 16);
+}
+
+// kv4_bf16x2 with the AND-OR in one operation (and_or).
+DLLM_DEV uint32_t kv4_bf16x2_masked(uint32_t w, int j, __nv_bfloat162 s, __nv_bfloat162 ms24, uint32_t mask) {
+  const uint32_t u = and_or<0x41804180u>(j == 0 ? w << 3 : w >> (4 * j - 3), mask);
+  const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), s, ms24);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 16-byte chunk c of row r of a 128-row tile of atoms (64 dims of 2 bytes) under the 128-byte swizzle.
+DLLM_DEV uint8_t* kv4_chunk(uint8_t* tile, int r, int c) {
+  return tile + (c >> 3) * 128 * 128 + r * 128 + (((c ^ r) & 7) << 4);
 }
 
 // Tile t's softmax: thread (warp w, lane) owns row 32 (w % 4) + lane of the tile.
 template <int HD>
-DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_t tmem_base, uint64_t* s_full,
+DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, const uint32_t* tmem_slot, uint64_t* s_full,
                                uint64_t* s_read, uint64_t* p_full, uint64_t* pv_done, uint64_t* q_full,
-                               uint8_t* q_smem, volatile int* flags,
-                               int t, int nt, int R0, int g, int sp, int ks, int ke, int nblk) {
+                               uint8_t* q_smem, volatile int* flags, int t, int R0, int g, int sp, int ks, int ke,
+                               int nblk) {
   using G = AttnKv4TcCfg<HD>;
-  constexpr int BK = G::BK, CH = G::CH, NCH = BK / CH;
+  constexpr int BK = G::BK, CH = G::CH, NCH = BK / CH, CHUNKS = HD / 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = 32 * (warp & 3) + lane;
-  const uint32_t lane_base = tmem_base + ((uint32_t)(32 * (warp & 3)) << 16);
-  const uint32_t s_col = lane_base + t * BK;
-  const uint32_t p_col = lane_base + G::kPCol + t * (BK / 2);
-  const uint32_t o_col = lane_base + G::kOCol + t * HD;
+  const int row0 = 32 * (warp & 3), row = row0 + lane;
   const int R = R0 + 128 * t + row;
   const bool real = R < rq.n * p.group;
   const int lim = real ? min(ke, kv4_row_limit(p, rq, R / p.group)) : ke;
-  // The thread's row of Q: to fp16, times a power of two that takes its largest magnitude to
-  // [2^14, 2^15) (attention_kv4.cuh), then 16-byte chunk c to column c ^ (row % 8) of its atom's
-  // 128-byte row. Rows past the last are 0.
-  float fac;   // from the sums of products with K's sixteenths to log2 weights
+  // Q: the warp's 32 rows, loaded along the rows; rows past the last are 0.
   {
-    uint4 q[HD / 8];
-    const bf16_t* src = p.q + (long)(rq.q0 + (real ? R / p.group : 0)) * p.q_tok + (g * p.group + (real ? R % p.group : 0)) * p.q_head;
-    uint32_t top = 0;
+    const long src = real ? (long)(rq.q0 + R / p.group) * p.q_tok + (g * p.group + R % p.group) * p.q_head : -1;
+    constexpr int BATCH = CHUNKS > 8 ? (CHUNKS + 1) / 2 : CHUNKS;   // loads in flight per thread
+#pragma unroll 1
+    for (int i0 = 0; i0 < CHUNKS; i0 += BATCH) {
+      uint4 q[BATCH];
 #pragma unroll
-    for (int c = 0; c < HD / 8; ++c) q[c] = real ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int c = 0; c < HD / 8; ++c) {
-      const uint32_t w[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-    }
-    const int up = 141 - max((int)(top >> 7), 15);
-    const float scale_q = __uint_as_float((uint32_t)(127 + up) << 23);
-    fac = __uint_as_float((uint32_t)(127 - up) << 23) * 16.f * p.scale_log2;
-#pragma unroll
-    for (int c = 0; c < HD / 8; ++c) {
-      uint32_t w[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __half2 v = __floats2half2_rn(__uint_as_float(w[e] << 16) * scale_q, __uint_as_float(w[e] & 0xFFFF0000u) * scale_q);
-        w[e] = *reinterpret_cast<const uint32_t*>(&v);
+      for (int i = 0; i < BATCH; ++i) {
+        const int u = 32 * (i0 + i) + lane, r = u / CHUNKS, c = u - r * CHUNKS;
+        const long from = __shfl_sync(0xffffffffu, src, r & 31);
+        q[i] = from >= 0 && r < 32 ? *reinterpret_cast<const uint4*>(p.q + from + 8 * c) : make_uint4(0, 0, 0, 0);
       }
-      *reinterpret_cast<uint4*>(q_smem + (c >> 3) * 128 * 128 + row * 128 + (((c ^ row) & 7) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int u = 32 * (i0 + i) + lane, r = u / CHUNKS, c = u - r * CHUNKS;
+        if (r < 32) *reinterpret_cast<uint4*>(kv4_chunk(q_smem, row0 + r, c)) = q[i];
+      }
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&q_full[t]);
   }
+  const float fac = p.scale_log2;
+  const uint32_t lane_base = *tmem_slot + ((uint32_t)row0 << 16);
+  const uint32_t s_col = lane_base + t * BK;
+  const uint32_t p_col = lane_base + G::kPCol + t * (BK / 2);
+  const uint32_t o_col = lane_base + G::kOCol + t * HD;
   float m = -INFINITY, l = 0.f;
   bool ok = true;
+#pragma unroll 1
   for (int j = 0; j < nblk; ++j) {
     if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], j & 1, flags))) { ok = false; break; }
     tc_fence_after();
     float s[CH];
     const int seen = lim - (ks + j * BK);
     auto load = [&](int q) {
-      kv4_load_scores<CH>(s_col + q * CH, s);
+      kv4_load_scores(s_col + q * CH, s);
       if (seen < (q + 1) * CH) {
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -241,7 +220,7 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_
         if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[t], (j - 1) & 1, flags))) { ok = false; break; }
         tc_fence_after();
       }
-      kv4_store_weights<CH>(p_col + q * (CH / 2), pk);
+      kv4_store_weights(p_col + q * (CH / 2), pk);
     }
     if (!ok) break;
     float l0, l1;
@@ -257,40 +236,52 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, uint32_
   tc_fence_after();
   const bool lost = flags[0] != 0 || flags[1] != 0;
   const float nan = __int_as_float(0x7FC00000);
-  const float inv = l == 0.f ? 0.f : 16.0f / l;   // V came in sixteenths
+  const float inv = lost ? nan : l == 0.f ? 0.f : 16.0f / l;   // V came in sixteenths
   const float lse2 = lost ? nan : l == 0.f ? -INFINITY : m + log2f(l);
-  const long tok = rq.q0 + R / p.group;
-  const int h = g * p.group + R % p.group;
+  // (where the row goes is worked out again, rather than kept in registers through the loop)
+  int row_now = R;
+  asm volatile("" : "+r"(row_now));
+  const long tok = rq.q0 + row_now / p.group;
+  const int h = g * p.group + row_now % p.group;
   const long at = ((long)sp * p.T + tok) * p.H + h;
-#pragma unroll 1
-  for (int c = 0; c < HD; c += 16) {
-    float v[16];
-    if (nblk > 0) {
-      tmem_ld16(o_col + c, v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = 0.f;
-    }
-    if (!real) continue;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = lost ? nan : l == 0.f ? 0.f : v[e] * inv;
-    if (p.n_splits == 1) {
-      uint32_t w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        w[e] = (uint32_t)f32_to_bf16_any(v[2 * e]) | ((uint32_t)f32_to_bf16_any(v[2 * e + 1]) << 16);
-      uint4* dst = reinterpret_cast<uint4*>(p.out + tok * p.o_tok + h * p.o_head + c);
-      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
-      float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + c);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-    }
-  }
   if (real) {
     if (p.n_splits > 1) p.part_lse[at] = lse2;
     else if (p.lse != nullptr) p.lse[tok * p.H + h] = lse2 * 0.6931471805599453f;
+  }
+  // O through the tile's Q, which no product reads any more, so that rows leave along the rows: bf16 in
+  // one go, fp32 partials in two halves of the dims
+  const bool whole = p.n_splits == 1;
+#pragma unroll 1
+  for (int half = 0; half < (whole ? 1 : 2); ++half) {
+    const int cols = whole ? HD : HD / 2;
+#pragma unroll 1
+    for (int at8 = 0; at8 < cols; at8 += 8) {
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (nblk > 0) tmem_ld8(o_col + half * (HD / 2) + at8, v);   // (without a block O was never written)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= inv;
+      if (whole) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = (uint32_t)f32_to_bf16_any(v[2 * e]) | ((uint32_t)f32_to_bf16_any(v[2 * e + 1]) << 16);
+        *reinterpret_cast<uint4*>(kv4_chunk(q_smem, row, at8 / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        *reinterpret_cast<float4*>(kv4_chunk(q_smem, row, at8 / 4)) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(kv4_chunk(q_smem, row, at8 / 4 + 1)) = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    }
+    __syncwarp();
+    uint8_t* to = whole ? reinterpret_cast<uint8_t*>(p.out + tok * p.o_tok + h * p.o_head)
+                        : reinterpret_cast<uint8_t*>(p.part_o + at * HD + half * (HD / 2));
+    if (!real) to = nullptr;
+#pragma unroll 2
+    for (int i = 0; i < CHUNKS; ++i) {
+      const int u = 32 * i + lane, r = u / CHUNKS, c = u - r * CHUNKS;
+      uint8_t* dst = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
+      if (dst != nullptr)
+        *reinterpret_cast<uint4*>(dst + 16 * c) = *reinterpret_cast<const uint4*>(kv4_chunk(q_smem, row0 + r, c));
+    }
+    __syncwarp();
   }
 }
 
@@ -301,7 +292,7 @@ __global__ void __launch_bounds__(AttnKv4TcCfg<HD>::THREADS, 1)
 attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
   using G = AttnKv4TcCfg<HD>;
   constexpr int BK = G::BK, AT = G::ATOMS, KST = G::KST, VST = G::VST;
-  constexpr uint32_t kIdQK = idesc_f16_f32(128, BK);
+  constexpr uint32_t kIdQK = idesc_bf16_f32(128, BK);
   constexpr uint32_t kIdPV = idesc_f16_f32(128, HD) | (1u << 16);   // B MN-major
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -359,21 +350,24 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     fence_mbar_init();
   }
   if (warp == 0) {
+    __syncwarp();
     tmem_alloc(tmem_slot, G::kTmemCols);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  pdl_trigger();   // after the TMEM allocation
-  const uint32_t tmem_base = *tmem_slot;
+  // Barriers and TMEM are there; the unpacking warps' first page ids are already on their way.
+  auto join = [&]() {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();   // after the TMEM allocation
+  };
 
-  if (warp < 4) {
-    regs_dec<G::kRegsIssue>();
+  if (warp < 2) {
+    join();
     if (warp < nt) {
       // ---------------- MMA issuer of tile `warp`: the warp waits as one, an elected lane issues
       const int t = __shfl_sync(0xffffffffu, warp, 0);
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
+      const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
       const uint32_t s_col = tm + t * BK, p_col = tm + G::kPCol + t * (BK / 2), o_col = tm + G::kOCol + t * HD;
       const uint64_t qd = sdesc_k_sw128(smem_u32(smem + t * G::kQTile));
       const uint64_t kd0 = sdesc_k_sw128(smem_u32(sK)), vd0 = sdesc_mn_sw128(smem_u32(sV), G::kAtom);
@@ -399,6 +393,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
         return true;
       };
       bool ok = nblk == 0 || (wait(&q_full[t], 0) && issue_s());
+#pragma unroll 1
       for (int j = 0; j < nblk && ok; ++j) {
         if (j + 1 < nblk && !(wait(&s_read[t], j & 1) && issue_s())) { ok = false; break; }
         if (!wait(&v_full[vst], vph) || !wait(&p_full[t], j & 1)) { ok = false; break; }
@@ -420,12 +415,11 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
       mbar_drain(&drain[t], 0);
       __syncwarp();
     }
-  } else if (warp >= 12) {
-    regs_dec<G::kRegsUnpack>();
+  } else if (warp >= 10) {
     // ---------------- unpacking: GPW times 8 keys of each block, lane / 4 the key, lane % 4 the group of an atom
     constexpr int GPW = G::GPW;
     const int k8 = lane >> 2, grp = lane & 3;
-    const int key0 = 8 * (warp - 12) + k8;                      // and key0 + 64
+    const int key0 = 8 * (warp - 10) + k8;                      // and key0 + 48
     const int* trow = p.table + (long)b * p.stride;
     const int mask = (1 << p.c.page_shift) - 1;
     const long v_rows = (long)p.c.Hkv << p.c.page_shift, page_rows = 2 * v_rows;
@@ -433,16 +427,21 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     uint2 code[2][GPW][AT];
     uint32_t byte[2][GPW][AT];
     int id_k[GPW], id_v[GPW];
-    // page id of a key in block j; -1 past the end, and for an id that is no page
-    auto pages = [&](int j, int (&id)[GPW]) {
+    // table entry of a key in block j, -2 past the end
+    auto ask = [&](int j, int (&id)[GPW]) {
 #pragma unroll
       for (int i = 0; i < GPW; ++i) {
-        const int t = ks + j * BK + key0 + 64 * i;
-        id[i] = -1;
-        if (j < nblk && t < ke) {
-          const int found = trow[t >> p.c.page_shift];
-          if (found >= 0 && found < p.c.n_pages) id[i] = found;
-          else flags[1] = 1;
+        const int t = ks + j * BK + key0 + 48 * i;
+        id[i] = j < nblk && t < ke ? trow[t >> p.c.page_shift] : -2;
+      }
+    };
+    // an entry that is no page becomes -1
+    auto check = [&](int (&id)[GPW]) {
+#pragma unroll
+      for (int i = 0; i < GPW; ++i) {
+        if (id[i] != -2 && (id[i] < 0 || id[i] >= p.c.n_pages)) {
+          id[i] = -1;
+          flags[1] = 1;
         }
       }
     };
@@ -450,7 +449,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     auto fetch = [&](int kv, int j, const int (&id)[GPW]) {
 #pragma unroll
       for (int i = 0; i < GPW; ++i) {
-        const long r = max(id[i], 0) * page_rows + (head_row + ((ks + j * BK + key0 + 64 * i) & mask)) + (kv ? v_rows : 0);
+        const long r = max(id[i], 0) * page_rows + (head_row + ((ks + j * BK + key0 + 48 * i) & mask)) + (kv ? v_rows : 0);
         const uint8_t* pc = p.c.codes + r * (HD / 2) + 8 * grp;
         const uint8_t* ps = p.c.scales + r * (HD / 16) + grp;
 #pragma unroll
@@ -466,14 +465,17 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     };
     const uint32_t at0 = key0 * 128 + (((2 * grp) ^ k8) << 4);
     const Kv4Masks masks{p.mask_low, p.mask_high};
-    bool ok = warp - 12 < G::UNPACK;
-    const bool works = ok;
+    bool ok = true;
     // K runs a block ahead of V, as S runs ahead of P V: the turns are K(0), K(1), V(0), K(2), V(1), ...
-    if (works) {
-      pages(0, id_v);
-      pages(1, id_k);
-      fetch(0, 0, id_v);
-    }
+    ask(0, id_v);
+    ask(1, id_k);
+    join();
+    check(id_v);
+    fetch(0, 0, id_v);
+    fetch(1, 0, id_v);
+    int kst = 0, vst = 0;            // stages, and the parities of their being empty
+    uint32_t kph = 1, vph = 1;
+#pragma unroll 1
     for (int j = -1; j < nblk && ok; ++j) {
       // this turn's bytes have had a block's time to arrive; all loads of the next one are issued
       // together before any is waited for again
@@ -490,20 +492,23 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
             scale[kv][i][a] = byte[kv][i][a];
             asm volatile("" : "+r"(now[kv][i][a].x), "+r"(now[kv][i][a].y), "+r"(scale[kv][i][a]));
           }
+      check(id_k);
       fetch(0, j + 2, id_k);
-      fetch(1, j + 1, id_v);
+      if (j >= 0) fetch(1, j + 1, id_v);
 #pragma unroll
       for (int i = 0; i < GPW; ++i) id_v[i] = id_k[i];
-      pages(j + 3, id_k);
+      ask(j + 3, id_k);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const int jb = kv ? j : j + 1;
         if (jb < 0 || jb >= nblk) continue;
-        const int n = kv ? VST : KST, st = jb % n;
-        if (!__all_sync(0xffffffffu, mbar_wait(&(kv ? v_empty : k_empty)[st], ((jb / n) & 1) ^ 1, flags))) {
+        const int st = kv ? vst : kst;
+        if (!__all_sync(0xffffffffu, mbar_wait(&(kv ? v_empty : k_empty)[st], kv ? vph : kph, flags))) {
           ok = false;
           break;
         }
+        if (kv == 0 && ++kst == KST) { kst = 0; kph ^= 1; }
+        if (kv == 1 && ++vst == VST) { vst = 0; vph ^= 1; }
         uint8_t* dst = (kv ? sV : sK) + st * G::kKV + at0;
         uint8_t* dst2 = (kv ? sV : sK) + st * G::kKV + (at0 ^ 16);
 #pragma unroll
@@ -511,12 +516,22 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
 #pragma unroll
           for (int a = 0; a < AT; ++a) {
             if (16 * (4 * a + grp) < HD) {
-              const Kv4Scale2 sc = kv4_scale2(scale[kv][i][a] * 0x00800080u);
               uint32_t o[8];
-              kv4_sixteenth(now[kv][i][a].x, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[0]));
-              kv4_sixteenth(now[kv][i][a].y, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[4]));
-              *reinterpret_cast<uint4*>(dst + a * G::kAtom + i * 64 * 128) = make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4*>(dst2 + a * G::kAtom + i * 64 * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+              if (kv == 0) {
+                const __nv_bfloat162 sc = kv4_scale_bf16x2(scale[kv][i][a]);
+                const __nv_bfloat162 m24 = __hmul2(sc, __float2bfloat162_rn(-24.f));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  o[e] = kv4_bf16x2_masked(now[kv][i][a].x, e, sc, m24, p.mask_bf16);
+                  o[4 + e] = kv4_bf16x2_masked(now[kv][i][a].y, e, sc, m24, p.mask_bf16);
+                }
+              } else {
+                const Kv4Scale2 sc = kv4_scale2(scale[kv][i][a] * 0x00800080u);
+                kv4_sixteenth(now[kv][i][a].x, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[0]));
+                kv4_sixteenth(now[kv][i][a].y, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[4]));
+              }
+              *reinterpret_cast<uint4*>(dst + a * G::kAtom + i * 48 * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(dst2 + a * G::kAtom + i * 48 * 128) = make_uint4(o[4], o[5], o[6], o[7]);
             }
           }
         fence_proxy_async_smem();
@@ -524,12 +539,13 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
         if (lane == 0) mbar_arrive(&(kv ? v_full : k_full)[st]);
       }
     }
-    if (works && !ok) flags[0] = 1;
+    if (!ok) flags[0] = 1;
   } else {
-    regs_inc<G::kRegsSoftmax>();
-    const int t = (warp - 4) >> 2;
+    join();
+    const int t = (warp - 2) >> 2;
     if (t < nt)
-      kv4_softmax_tile<HD>(p, rq, tmem_base, s_full, s_read, p_full, pv_done, q_full, smem + t * G::kQTile, flags, t, nt, R0, g, sp, ks, ke, nblk);
+      kv4_softmax_tile<HD>(p, rq, tmem_slot, s_full, s_read, p_full, pv_done, q_full, smem + t * G::kQTile, flags, t, R0, g, sp,
+                           ks, ke, nblk);
   }
   __syncwarp();
   tc_fence_before();
@@ -537,7 +553,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
   tc_fence_after();
   if (warp == 0) {
     __syncwarp();
-    tmem_dealloc(tmem_base, G::kTmemCols);
+    tmem_dealloc(*tmem_slot, G::kTmemCols);
   }
 }
 

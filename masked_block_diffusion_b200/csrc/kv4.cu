@@ -123,6 +123,9 @@ AttnPlan attn_plan(int B, int max_q, int max_kv, int group, int Hkv, int hd) {
   const long blocks = (long)B * Hkv * a.tiles;
   long want;
   if (a.nr == 0) {
+    // As many as still run at once. 256 queries over 2048 keys (16 blocks): 1 split 106 us, 2 64, 4 42, 8 31, 9 (this
+    // rule) 30, 12 47. Two splits of calls that fill the GPU are no faster: 16 such canvases 184 -> 244 us, and three
+    // prompt pieces, the longest of 1024 queries over 4096 keys, 125 -> 124.
     want = slots / blocks;
   } else if (blocks * ceil_div(max_kv, 256) <= slots) {
     want = ceil_div(max_kv, 256);                      // a short call: as wide as it goes
@@ -132,7 +135,7 @@ AttnPlan attn_plan(int B, int max_q, int max_kv, int group, int Hkv, int hd) {
     want = blocks >= slots / 4 ? std::min<long>(ceil_div(2 * slots, blocks), ceil_div(max_kv, 512)) : slots / blocks;
   }
   want = std::max(1L, std::min<long>(want, ceil_div(max_kv, a.nr ? 64 : 128)));
-  const int grain = a.nr ? 128 : hd == 64 ? 128 : hd == 128 ? 64 : 48;   // keys of a kernel's stage or block
+  const int grain = a.nr ? 128 : hd == 64 ? 96 : 48;   // keys of a kernel's stage or block
   a.chunk = std::max(grain, ceil_div(ceil_div(max_kv, want), grain) * grain);
   a.n_splits = std::max(1, ceil_div(max_kv, a.chunk));
   return a;
@@ -173,7 +176,11 @@ template <int HD>
 cudaError_t run_attn(cudaStream_t st, const AttnPlan& a, const AttnKv4Params& p) {
   cudaError_t e = a.nr == 1 ? run_few<HD, 1>(st, a, p) : a.nr == 2 ? run_few<HD, 2>(st, a, p) : run_tc<HD>(st, a, p);
   if (e == cudaSuccess && a.n_splits > 1)
-    e = launch(st, attn_kv4_merge_kernel<HD>, dim3((unsigned)p.max_q * p.H, p.B), 128, 0, p);
+    // Many rows: a warp per row (256 queries of 16 heads in 9 splits: 33.3 us with a block per row, 30.4 with a
+    // warp). A few: a block per row, whose warps share the splits (16 rows in 17 splits: 12.1 us, 13.6 with a warp).
+    e = a.nr == 0 && a.n_splits <= 32
+            ? launch(st, attn_kv4_merge_rows_kernel<HD>, dim3(ceil_div((long)p.max_q * p.H, 8), p.B), 256, 0, p)
+            : launch(st, attn_kv4_merge_kernel<HD>, dim3((unsigned)p.max_q * p.H, p.B), 128, 0, p);
   return e;
 }
 
@@ -351,6 +358,7 @@ int dllm_op_attn_kv4(const dllm_kv4* cache, const uint16_t* q, long long q_token
   p.scale_log2 = scale * 1.4426950408889634f;
   p.mask_low = 0x003C003Cu;
   p.mask_high = 0x03C003C0u;
+  p.mask_bf16 = 0x00780078u;
   p.part_o = reinterpret_cast<float*>(workspace);
   p.part_lse = p.part_o + (size_t)a.n_splits * T * H * cache->head_dim;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
