@@ -394,7 +394,8 @@ int dllm_op_read_kv4(const dllm_kv4* cache, const int32_t* req, const int32_t* p
  *   lse[t][h] (fp32 [T][H], or NULL) = the natural log of the sum of exp(scale * q k), -inf for a
  *   row that sees no key: it joins this result with attention over other keys.
  * Rows of q that no request covers are left as they were in out and lse. max_q and max_kv are the
- * caller's bounds on the requests' queries and keys (max_q <= T, max_kv < 2^29). A request that
+ * caller's bounds on the requests' queries and keys (max_q <= T, max_kv < 2^29; nothing is
+ * queued if max_q or B is 0). out may be q itself, with equal strides. A request that
  * exceeds them or its row of the table, or with kv_len < 0, gets NaN in all its rows; one whose
  * q_start range is not within 0 .. T is skipped; a page id outside the cache gives NaN in the
  * rows that see it (other rows of that request may be NaN too), as does a kernel that gives

@@ -83,14 +83,13 @@ def _ints(name: str, t: torch.Tensor, dev: int, n: int) -> int:
 
 
 def _table(t: torch.Tensor, dev: int) -> tuple:
-    """(address, rows, row stride)"""
+    """(address, rows, columns)"""
     if t.dtype is not torch.int32 or t.dim() != 2 or t.get_device() != dev:
         _bad("table", f"expected int32 [requests][pages] on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     rows, cols = t.shape
-    sr, sc = t.stride()
-    if rows < 1 or cols < 1 or (cols > 1 and sc != 1):
-        _bad("table", f"expected at least one row and page, and contiguous rows: {tuple(t.shape)}")
-    return t.data_ptr(), rows, sr if rows > 1 else cols
+    if rows < 1 or cols < 1 or not t.is_contiguous():   # (a slice's row stride would be taken for its width)
+        _bad("table", f"expected a contiguous tensor of at least one row and page, got {tuple(t.shape)}")
+    return t.data_ptr(), rows, cols
 
 
 def _refuse_grad() -> None:
@@ -240,7 +239,8 @@ class KVCache4:
         it sees positions below kv_len[b] of table row b; causal: its queries are the last of
         those. max_q, max_kv: bounds on a request's queries and keys. scale: 1 / sqrt(head_dim)
         by default. workspace: a uint8 tensor of workspace_bytes(...) for callers that allocate
-        nothing here. Returns out (bf16, q's shape), with return_lse (out, lse fp32 [T][heads])."""
+        nothing here. Returns out (bf16, q's shape), with return_lse (out, lse fp32 [T][heads]); rows
+        that no request covers are left as they were, so they hold anything in tensors made here."""
         if q.dim() != 3:
             _bad("q", f"expected [T][heads][head_dim], got {tuple(q.shape)}")
         T, H, hd = q.shape

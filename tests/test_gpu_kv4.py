@@ -202,6 +202,35 @@ def test_append_stores_the_defined_bytes(d, hk, page, tin, aligned):
     assert np.array_equal(f64(k), held[0]) and np.array_equal(f64(v), held[1])
 
 
+@pytest.mark.parametrize("tin", [torch.float32, torch.bfloat16])
+def test_append_at_every_scale(tin):
+    """Values at, just above and just below the ties between codes, and largest values just above and below
+    what a scale holds, for every scale: the nearest code of the exact quotient."""
+    s = ref.scale_values()[1:ref.MAX_SCALE_BYTE + 1].astype(np.float32)
+    ties = np.append(np.arange(-7, 8) + 0.5, 7.0).astype(np.float32)[None] * s[:, None]    
+    ties[:, 14] = 0.0                                                # in place of 7.5, which no group holds
+    up, down = np.nextafter(ties, np.float32(np.inf)), np.nextafter(ties, np.float32(-np.inf))
+    up[:, 15] = down[:, 15] = ties[:, 15]
+    over = down.copy()
+    over[:, 15] = np.nextafter(ties[:, 15], np.float32(np.inf))       # the next scale is due (the last one saturates)
+    k = np.stack([ties, up, down, over], 1).reshape(-1, 1, 64)
+    rng = np.random.default_rng(3)
+    v = (rng.uniform(-7, 7, (len(s), 4, 16)) * s[:, None, None]).astype(np.float32)
+    v[:, 0, 0] = np.nextafter(7 * s, np.float32(0))
+    v = v.reshape(-1, 1, 64)
+    kv = torch.tensor(np.stack([k, v]), device="cuda").to(tin)
+    n = len(s)
+    c = fresh(-(-n // 16), 16, 1, 64)
+    table = np.arange(c.n_pages)[None]
+    pos = np.arange(n)
+    c.append(kv[0], kv[1], i32(np.zeros(n)), i32(pos), i32(table))
+    codes, byte = ref.quantise(f64(kv))
+    want = ref.pack(codes)
+    for part in (0, 1):
+        assert np.array_equal(c.scales.cpu().numpy()[pos // 16, part, :, pos % 16], byte[part])
+        assert np.array_equal(c.codes.cpu().numpy()[pos // 16, part, :, pos % 16], want[part])
+
+
 @pytest.mark.parametrize("layout,rotary,scaling", [("half", 176, {}), ("interleaved", 64, {}), ("half", 60, {}),
                                                    ("interleaved", 6, dict(scaling="yarn", factor=8.0, original_ctx=512))])
 @pytest.mark.parametrize("tin", [torch.float32, torch.bfloat16])
@@ -356,6 +385,23 @@ def test_attention_split_over_a_long_cache(d, h, hk):
 
 def test_attention_split_canvas():
     attend_case(176, 4, 2, 64, [40, 17], [3001, 1290], False, seed=21)
+
+
+@pytest.mark.parametrize("d,keys", [(64, 10000), (128, 5000), (176, 7000)])
+def test_attention_of_one_tile_in_many_splits(d, keys):
+    """One KV head and few rows: more splits than a warp has lanes."""
+    attend_case(d, 2, 1, 64, [20], [keys], True, seed=22)
+
+
+@pytest.mark.parametrize("queries", [1, 30])
+def test_attention_without_a_key_and_in_place(queries):
+    cache, table, held = filled(np.random.default_rng(23), [70], 16, 2, 64)
+    q = torch.randn(queries, 8, 64, device="cuda").bfloat16()
+    out, lse = cache.attend(q, i32([0, queries]), i32([0]), i32(table), max_q=queries, max_kv=0, return_lse=True)
+    assert not out.any() and (lse == -np.inf).all()
+    want = cache.attend(q, i32([0, queries]), i32([70]), i32(table), max_q=queries, max_kv=70)
+    assert cache.attend(q, i32([0, queries]), i32([70]), i32(table), max_q=queries, max_kv=70, out=q) is q
+    assert torch.equal(q, want)
 
 
 def test_attention_with_scores_that_climb_and_with_one_that_stands_out():
@@ -597,7 +643,8 @@ def test_torch_refusals():
     req, pos = i32([0, 0, 0]), i32([0, 1, 2])
     for bad in (lambda: c.attend(q.float(), start, lens, tab, 3, 10), lambda: c.attend(q[..., :32], start, lens, tab, 3, 10),
                 lambda: c.attend(q, start[:1], lens, tab, 3, 10), lambda: c.attend(q, start, lens.long(), tab, 3, 10),
-                lambda: c.attend(q, start, lens, tab[0], 3, 10), lambda: c.attend(q, i32([0, 1, 3]), i32([5, 5]), tab, 3, 10),
+                lambda: c.attend(q, start, lens, tab[0], 3, 10), lambda: c.attend(q, start, lens, tab.expand(2, 1), 3, 10),
+                lambda: c.attend(q, start, lens, i32([[0, 1], [2, 3]])[:, :1], 3, 10), lambda: c.attend(q, i32([0, 1, 3]), i32([5, 5]), tab, 3, 10),
                 lambda: c.attend(q, start, lens, tab, 3, 10, out=torch.zeros_like(q, dtype=torch.float32)),
                 lambda: c.append(k, k.bfloat16(), req, pos, tab), lambda: c.append(k[:, :1], k, req, pos, tab),
                 lambda: c.append(k, k, req[:2], pos, tab), lambda: c.append(k, k, req, pos.float(), tab),
@@ -613,3 +660,42 @@ def test_torch_refusals():
     assert c.attend(q[:0], i32([0, 0]), lens, tab, 0, 10).shape == (0, 4, 64)
     assert c.read(req[:0], pos[:0], tab)[0].shape == (0, 2, 64)
     c.append(k[:0], k[:0], req[:0], pos[:0], tab)
+
+
+@pytest.mark.parametrize("d,queries", [(64, 1), (176, 1), (64, 40), (176, 256)])
+def test_a_wait_that_runs_out_answers_nan_and_the_next_call_is_right(d, queries):
+    """Waits limited to 1 ns, a first wait of up to 256 ns aside: rows are lost as a whole or right. Only the last of
+    these calls has waits that take long enough in every run: many blocks at once, out of the L2 cache."""
+    from masked_block_diffusion_b200 import Denoiser
+    from synth import WORKLOADS, blob_from_weights, gen_weights
+
+    cfg = WORKLOADS["c1-tiny-dense"].model
+    den = Denoiser(cfg, blob_from_weights(cfg, gen_weights(cfg)), max_ctx=256, max_batch=1)
+    n, keys, page = 80, 3000, 64
+    rng = np.random.default_rng(24)
+    cache, table, held = filled(rng, [keys] * 4, page, 2, d)
+    q = torch.tensor(2.0 * rng.normal(size=(n * queries, 4, d)), device="cuda").bfloat16()
+    args = (q, i32(np.arange(n + 1) * queries), i32([keys] * n), i32(np.tile(table, (n // 4, 1))), queries, keys)
+    out, lse = cache.attend(*args, return_lse=True)
+    check_attention(out[:queries], lse[:queries], q, held, [queries], [keys], False, d ** -0.5)
+    big = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    seen = False
+    torch.cuda.synchronize()
+    try:
+        binding.dllm_set_wait_limit(den.h, 1)
+        try:
+            for i in range(10):
+                big.fill_(i)
+                o, z = cache.attend(*args, return_lse=True)
+                lost = torch.isnan(z)
+                seen = seen or bool(lost.any())
+                assert torch.equal(lost, torch.isnan(o).all(-1)) and torch.equal(lost, torch.isnan(o).any(-1))
+                assert torch.equal(o[~lost], out[~lost]) and torch.equal(z[~lost], lse[~lost])
+        finally:
+            torch.cuda.synchronize()
+            binding.dllm_set_wait_limit(den.h, 0)
+        assert seen or (d, queries) != (176, 256)
+        o, z = cache.attend(*args, return_lse=True)
+        assert torch.equal(o, out) and torch.equal(z, lse)
+    finally:
+        den.close()
