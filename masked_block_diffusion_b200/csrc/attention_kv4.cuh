@@ -46,10 +46,14 @@ struct AttnKv4Params {
   const int* table;         // [B][stride]
   int stride, B, T, H, group;
   int max_q, max_kv, causal;
-  int n_splits, chunk;      // keys [i chunk, (i + 1) chunk) belong to split i; chunk % 64 == 0
+  int n_splits, chunk;      // keys [i chunk, (i + 1) chunk) belong to split i
   float scale_log2;         // scale * log2(e)
   float* part_o;            // [n_splits][T][H][hd]
   float* part_lse;          // [n_splits][T][H], log2 domain
+  // On tcgen05 instead, two per block of the grid: part_o [2 blocks][hd / 4][256 rows][4], part_lse [2 blocks][256], and
+  // parts[i] = (request, KV head, tile, 1: goes on in the next block, 2: ends here; 0: no such part)
+  int4* parts;
+  int cut;                  // 0: tiles stay whole, and there are no parts
   uint32_t mask_low, mask_high;   // Kv4Masks
   uint32_t mask_bf16;             // 0x00780078
 };
@@ -78,9 +82,9 @@ DLLM_DEV int kv4_row_limit(const AttnKv4Params& p, const Kv4Req& r, int query) {
 }
 
 // Every row of a bad request's head range [h0, h0 + nh) becomes NaN.
-DLLM_DEV void kv4_poison(const AttnKv4Params& p, const Kv4Req& r, int h0, int nh, int hd) {
+DLLM_DEV void kv4_poison(const AttnKv4Params& p, const Kv4Req& r, int h0, int nh, int hd, int first, int step) {
   const long total = (long)r.n * nh * hd;
-  for (long u = threadIdx.x; u < total; u += blockDim.x) {
+  for (long u = first; u < total; u += step) {
     const long row = u / hd;
     const long t = r.q0 + row / nh;
     const int h = h0 + (int)(row % nh), d = (int)(u - row * hd);
@@ -191,7 +195,7 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
   const int R0 = tile * G::kRows, n_rows = rq.n * p.group;
   if (rq.skip) return;
   if (rq.bad) {
-    if (tile == 0 && sp == 0) kv4_poison(p, rq, g * p.group, p.group, HD);
+    if (tile == 0 && sp == 0) kv4_poison(p, rq, g * p.group, p.group, HD, threadIdx.x, blockDim.x);
     return;
   }
   if (R0 >= n_rows) return;
@@ -589,58 +593,6 @@ attn_kv4_merge_kernel(const __grid_constant__ AttnKv4Params p) {
   }
   if (threadIdx.x == 0 && p.lse != nullptr)
     p.lse[t * p.H + h] = nan ? qnan : mx == -INFINITY ? -INFINITY : (mx + log2f(all)) * 0.6931471805599453f;
-}
-
-// The same for up to 32 splits of many rows: one warp per query and head, which has all of a few splits'
-// loads in flight; eight rows a block. Grid (ceil(max_q * H / 8), B).
-template <int HD>
-__global__ void __launch_bounds__(256)
-attn_kv4_merge_rows_kernel(const __grid_constant__ AttnKv4Params p) {
-  constexpr int VI = (HD + 127) / 128;
-  pdl_begin();
-  const int u = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int i = u / p.H, h = u - i * p.H;
-  const Kv4Req rq = kv4_request(p, blockIdx.y);
-  if (rq.skip || rq.bad || i >= rq.n) return;
-  const long at = (long)(rq.q0 + i) * p.H + h;
-  const long row = (long)p.T * p.H;
-  const float lse = lane < p.n_splits ? p.part_lse[lane * row + at] : -INFINITY;
-  float mx = lse;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const bool nan = __any_sync(0xffffffffu, lse != lse);
-  const float w = exp2f(lse - (mx == -INFINITY ? 0.f : mx));
-  const float all = warp_sum(w);
-  float4 acc[VI];
-#pragma unroll
-  for (int v = 0; v < VI; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float* po = p.part_o + at * HD + 4 * lane;
-#pragma unroll 4
-  for (int s = 0; s < p.n_splits; ++s) {
-    const float ws = __shfl_sync(0xffffffffu, w, s);
-#pragma unroll
-    for (int v = 0; v < VI; ++v) {
-      if (128 * v + 4 * lane < HD) {
-        const float4 x = *reinterpret_cast<const float4*>(po + s * row * HD + 128 * v);
-        acc[v].x += ws * x.x;
-        acc[v].y += ws * x.y;
-        acc[v].z += ws * x.z;
-        acc[v].w += ws * x.w;
-      }
-    }
-  }
-  const float inv = nan ? __int_as_float(0x7FC00000) : mx == -INFINITY ? 0.f : 1.f / all;
-#pragma unroll
-  for (int v = 0; v < VI; ++v) {
-    const int d = 128 * v + 4 * lane;
-    if (d < HD) {
-      const uint32_t a = (uint32_t)f32_to_bf16_any(acc[v].x * inv) | ((uint32_t)f32_to_bf16_any(acc[v].y * inv) << 16);
-      const uint32_t b = (uint32_t)f32_to_bf16_any(acc[v].z * inv) | ((uint32_t)f32_to_bf16_any(acc[v].w * inv) << 16);
-      *reinterpret_cast<uint2*>(p.out + (rq.q0 + i) * p.o_tok + h * p.o_head + d) = make_uint2(a, b);
-    }
-  }
-  if (lane == 0 && p.lse != nullptr)
-    p.lse[at] = nan ? __int_as_float(0x7FC00000) : mx == -INFINITY ? -INFINITY : (mx + log2f(all)) * 0.6931471805599453f;
 }
 
 }  // namespace dllm

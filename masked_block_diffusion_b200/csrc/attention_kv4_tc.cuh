@@ -74,6 +74,7 @@ struct AttnKv4TcCfg {
   static constexpr int UNPACK = 6;                       // unpacking warps
   static constexpr int GPW = BK / 8 / UNPACK;            // groups of 8 keys of a block that each takes
   static constexpr int THREADS = 32 * (2 + 8 + UNPACK);
+  static constexpr int START = 4;                        // what starting a tile costs, in blocks of keys
   static_assert(kOCol + 2 * HD <= kTmemCols, "TMEM");
   static_assert(kTotal <= 232448, "shared memory");
   static_assert(kOffBar % 16 == 0, "barriers");
@@ -102,43 +103,173 @@ DLLM_DEV uint32_t kv4_bf16x2_masked(uint32_t w, int j, __nv_bfloat162 s, __nv_bf
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// 16 bytes from global to shared memory, `n` of them (0 or 16) read and the others 0.
+DLLM_DEV void copy16(void* dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
+               "l"((uint64_t)__cvta_generic_to_global(src)), "r"(n)
+               : "memory");
+}
+
 // 16-byte chunk c of row r of a 128-row tile of atoms (64 dims of 2 bytes) under the 128-byte swizzle.
 DLLM_DEV uint8_t* kv4_chunk(uint8_t* tile, int r, int c) {
   return tile + (c >> 3) * 128 * 128 + r * 128 + (((c ^ r) & 7) << 4);
 }
 
-// Tile t's softmax: thread (warp w, lane) owns row 32 (w % 4) + lane of the tile.
+// a / b for a >= 0, b > 0: in 32 bits where they fit, since every thread does it and 64 bits take ten times as long.
+DLLM_DEV long kv4_div(long a, long b) { return (a | b) >> 32 ? a / b : (long)((uint32_t)a / (uint32_t)b); }
+
+// A row tile over key blocks j0 .. j1 - 1.
+struct Kv4Work {
+  int b, h, tile, j0, j1;
+  bool starts, ends;        // with the tile's first, last key block
+  Kv4Req rq;
+};
+
+// The work of a thread block, the same in all its threads: a share of all tiles' key blocks, which lie
+// request by request, head by head, from the last tile (which sees the most keys when causal) to the
+// first. Lengths are known on the device only, so each block adds up the requests' work by itself
+// (begin). If the caller's bounds say that tiles are short (cut = 0), the shares are of whole tiles. Else they are equal: 16 requests of 256 queries over 2176 to 4352 keys, 256 tiles on
+// 148 SMs, @@. With fewer tiles than blocks, each tile has as many shares as fit: one canvas, 16
+// tiles, in 9 shares each (shares that cut across tiles as well: @@).
 template <int HD>
-DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, const uint32_t* tmem_slot, uint64_t* s_full,
+struct Kv4Walk {
+  using G = AttnKv4TcCfg<HD>;
+  int b, h, i, x;           // the next tile, and how far into it the share begins
+  long left;
+  int tiles;
+  Kv4Req rq;
+
+  DLLM_DEV int blocks(const AttnKv4Params& p, int tile) const {
+    if (rq.bad) return 0;
+    const int last = min(rq.n * p.group, 256 * (tile + 1)) - 1;
+    return (kv4_row_limit(p, rq, last / p.group) + G::BK - 1) / G::BK;
+  }
+  DLLM_DEV void request(const AttnKv4Params& p, int b_) {
+    b = b_;
+    rq = kv4_request(p, b);
+    tiles = rq.bad ? rq.n > 0 : (rq.n * p.group + 255) / 256;   // a bad request is answered with its first tile
+  }
+  DLLM_DEV int cost(const AttnKv4Params& p, int tile) const { return p.cut ? G::START + blocks(p, tile) : 1; }
+  DLLM_DEV long costs(const AttnKv4Params& p) const {
+    if (!p.cut) return tiles;
+    long c = 0;
+    for (int t = 0; t < tiles; ++t) c += cost(p, t);
+    return c;
+  }
+  // All threads; mem: 16 bytes and 16 per warp, free again after the next barrier.
+  DLLM_DEV void begin(const AttnKv4Params& p, long* mem) {
+    constexpr int WARPS = G::THREADS / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int r0 = (int)((long)p.B * tid / G::THREADS), r1 = (int)((long)p.B * (tid + 1) / G::THREADS);
+    long mine = 0, some = 0;
+    for (int r = r0; r < r1; ++r) {
+      request(p, r);
+      mine += p.c.Hkv * costs(p);
+      some += p.c.Hkv * tiles;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) some += __shfl_xor_sync(0xffffffffu, some, o);
+    long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) {
+      mem[warp] = upto;
+      mem[WARPS + warp] = some;
+    }
+    int* found = reinterpret_cast<int*>(mem + 2 * WARPS);
+    __syncthreads();
+    long all = 0, count = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      upto += w < warp ? mem[w] : 0;
+      all += mem[w];
+      count += mem[WARPS + w];
+    }
+    // no share is empty but the last blocks', so that a tile's parts lie in consecutive blocks
+    long n = min(all, (long)gridDim.x);
+    if (count > 0 && count < n) n = kv4_div(n, count) * count;
+    const long k = min((long)blockIdx.x, n);
+    const long lo = n > 0 ? kv4_div(all * k, n) : 0;
+    left = k < n ? kv4_div(all * (k + 1), n) - lo : 0;
+    if (lo >= upto - mine && lo < upto) {
+      long rest = lo - (upto - mine);
+      for (int r = r0; r < r1; ++r) {
+        request(p, r);
+        const long c = costs(p);
+        if (rest >= p.c.Hkv * c) {
+          rest -= p.c.Hkv * c;
+          continue;
+        }
+        found[0] = r;
+        found[1] = (int)kv4_div(rest, c);
+        rest -= found[1] * c;
+        int t = tiles - 1;
+        for (int c1 = cost(p, t); rest >= c1; c1 = cost(p, --t)) rest -= c1;
+        found[2] = t;
+        found[3] = (int)rest;
+        break;
+      }
+    }
+    __syncthreads();
+    if (left > 0) {
+      request(p, found[0]);
+      h = found[1];
+      i = found[2];
+      x = found[3];
+    }
+  }
+  DLLM_DEV bool next(const AttnKv4Params& p, Kv4Work& w) {
+    while (left > 0) {
+      if (i < 0) {
+        if (++h == p.c.Hkv) {
+          h = 0;
+          if (++b >= p.B) return false;
+          request(p, b);
+        }
+        i = tiles - 1;
+        continue;
+      }
+      const int all = blocks(p, i), take = (int)min(left, (long)(cost(p, i) - x));
+      const int j0 = p.cut ? max(0, x - G::START) : 0, j1 = p.cut ? max(0, x + take - G::START) : all;
+      const bool begun = x == 0;
+      w = Kv4Work{b, h, i, j0, j1, j0 == 0, j1 == all, rq};
+      left -= take;
+      --i;
+      x = 0;
+      if (j1 > j0 || (all == 0 && begun)) return true;
+    }
+    return false;
+  }
+};
+
+// Tile t's softmax: thread (warp w, lane) owns row 32 (w % 4) + lane of the tile. `done` counts the blocks of
+// keys that went through the tile's barriers before.
+template <int HD>
+DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const uint32_t* tmem_slot, uint64_t* s_full,
                                uint64_t* s_read, uint64_t* p_full, uint64_t* pv_done, uint64_t* q_full,
-                               uint8_t* q_smem, volatile int* flags, int t, int R0, int g, int sp, int ks, int ke,
-                               int nblk) {
+                               uint8_t* q_smem, volatile int* flags, int t, uint32_t done) {
   using G = AttnKv4TcCfg<HD>;
   constexpr int BK = G::BK, CH = G::CH, NCH = BK / CH, CHUNKS = HD / 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = 32 * (warp & 3), row = row0 + lane;
-  const int R = R0 + 128 * t + row;
+  const int R = 256 * w.tile + 128 * t + row;
+  const Kv4Req& rq = w.rq;
+  const int g = w.h, nblk = w.j1 - w.j0, ks = w.j0 * BK, ke = w.j1 * BK;
   const bool real = R < rq.n * p.group;
   const int lim = real ? min(ke, kv4_row_limit(p, rq, R / p.group)) : ke;
-  // Q: the warp's 32 rows, loaded along the rows; rows past the last are 0.
+  // Q: the warp's 32 rows, copied along the rows; rows past the last are 0
   {
     const long src = real ? (long)(rq.q0 + R / p.group) * p.q_tok + (g * p.group + R % p.group) * p.q_head : -1;
-    constexpr int BATCH = CHUNKS > 8 ? (CHUNKS + 1) / 2 : CHUNKS;   // loads in flight per thread
-#pragma unroll 1
-    for (int i0 = 0; i0 < CHUNKS; i0 += BATCH) {
-      uint4 q[BATCH];
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        const int u = 32 * (i0 + i) + lane, r = u / CHUNKS, c = u - r * CHUNKS;
-        const long from = __shfl_sync(0xffffffffu, src, r & 31);
-        q[i] = from >= 0 && r < 32 ? *reinterpret_cast<const uint4*>(p.q + from + 8 * c) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        const int u = 32 * (i0 + i) + lane, r = u / CHUNKS, c = u - r * CHUNKS;
-        if (r < 32) *reinterpret_cast<uint4*>(kv4_chunk(q_smem, row0 + r, c)) = q[i];
-      }
+#pragma unroll 2
+    for (int i = 0; i < CHUNKS; ++i) {
+      const int u = 32 * i + lane, r = u / CHUNKS, c = u - r * CHUNKS;
+      const long from = __shfl_sync(0xffffffffu, src, r);
+      copy16(kv4_chunk(q_smem, row0 + r, c), p.q + (from >= 0 ? from + 8 * c : 0), from >= 0 ? 16 : 0);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&q_full[t]);
@@ -152,7 +283,7 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, const u
   bool ok = true;
 #pragma unroll 1
   for (int j = 0; j < nblk; ++j) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], j & 1, flags))) { ok = false; break; }
+    if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], (done + j) & 1, flags))) { ok = false; break; }
     tc_fence_after();
     float s[CH];
     const int seen = lim - (ks + j * BK);
@@ -178,7 +309,7 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, const u
       const bool need = mx > m + (kKv4Low + 8.f);
       if (__any_sync(0xffffffffu, need)) {
         // O is stable once the product of the block before is done
-        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[t], (j - 1) & 1, flags))) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[t], (done + j - 1) & 1, flags))) { ok = false; break; }
         tc_fence_after();
         const float mn = need ? mx - kKv4Low : m;
         const float f = need ? exp2f(m - mn) : 1.0f;
@@ -217,7 +348,7 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, const u
         pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
       }
       if (q == NCH - 1 && j > 0) {   // P's columns are free once the product of the block before is done
-        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[t], (j - 1) & 1, flags))) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[t], (done + j - 1) & 1, flags))) { ok = false; break; }
         tc_fence_after();
       }
       kv4_store_weights(p_col + q * (CH / 2), pk);
@@ -231,10 +362,10 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, const u
     __syncwarp();
     if (lane == 0) mbar_arrive(&p_full[t]);
   }
-  if (ok && nblk > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], (nblk - 1) & 1, flags));
+  if (ok && nblk > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], (done + nblk - 1) & 1, flags));
   if (!ok) flags[0] = 1;
   tc_fence_after();
-  const bool lost = flags[0] != 0 || flags[1] != 0;
+  const bool lost = flags[0] != 0;
   const float nan = __int_as_float(0x7FC00000);
   const float inv = lost ? nan : l == 0.f ? 0.f : 16.0f / l;   // V came in sixteenths
   const float lse2 = lost ? nan : l == 0.f ? -INFINITY : m + log2f(l);
@@ -243,50 +374,50 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Req& rq, const u
   asm volatile("" : "+r"(row_now));
   const long tok = rq.q0 + row_now / p.group;
   const int h = g * p.group + row_now % p.group;
-  const long at = ((long)sp * p.T + tok) * p.H + h;
-  if (real) {
-    if (p.n_splits > 1) p.part_lse[at] = lse2;
-    else if (p.lse != nullptr) p.lse[tok * p.H + h] = lse2 * 0.6931471805599453f;
-  }
-  // O through the tile's Q, which no product reads any more, so that rows leave along the rows: bf16 in
-  // one go, fp32 partials in two halves of the dims
-  const bool whole = p.n_splits == 1;
+  // a part of a tile: the block's second one if it is the tile's first (then it is the block's last work)
+  const int part = 2 * blockIdx.x + w.starts;
+  if (!(w.starts && w.ends)) {
+    p.part_lse[part * 256 + 128 * t + row] = lse2;
+    if (t == 0 && row == 0) p.parts[part] = make_int4(w.b, w.h, w.tile, w.ends ? 2 : 1);
+    float4* to = reinterpret_cast<float4*>(p.part_o) + (long)part * 64 * HD + 128 * t + row;
 #pragma unroll 1
-  for (int half = 0; half < (whole ? 1 : 2); ++half) {
-    const int cols = whole ? HD : HD / 2;
-#pragma unroll 1
-    for (int at8 = 0; at8 < cols; at8 += 8) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (nblk > 0) tmem_ld8(o_col + half * (HD / 2) + at8, v);   // (without a block O was never written)
+    for (int c = 0; c < HD; c += 16) {
+      float v[16];
+      tmem_ld16(o_col + c, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= inv;
-      if (whole) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = (uint32_t)f32_to_bf16_any(v[2 * e]) | ((uint32_t)f32_to_bf16_any(v[2 * e + 1]) << 16);
-        *reinterpret_cast<uint4*>(kv4_chunk(q_smem, row, at8 / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-        *reinterpret_cast<float4*>(kv4_chunk(q_smem, row, at8 / 4)) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(kv4_chunk(q_smem, row, at8 / 4 + 1)) = make_float4(v[4], v[5], v[6], v[7]);
-      }
+      for (int e = 0; e < 16; e += 4)
+        to[(c + e) * 64] = make_float4(v[e] * inv, v[e + 1] * inv, v[e + 2] * inv, v[e + 3] * inv);
     }
-    __syncwarp();
-    uint8_t* to = whole ? reinterpret_cast<uint8_t*>(p.out + tok * p.o_tok + h * p.o_head)
-                        : reinterpret_cast<uint8_t*>(p.part_o + at * HD + half * (HD / 2));
-    if (!real) to = nullptr;
+    return;
+  }
+  if (real && p.lse != nullptr) p.lse[tok * p.H + h] = lse2 * 0.6931471805599453f;
+  // O through the tile's Q, which no product reads any more, so that rows leave along the rows
+#pragma unroll 1
+  for (int c = 0; c < HD; c += 16) {
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = 0.f;
+    if (nblk > 0) tmem_ld16(o_col + c, v);   // (without a block O was never written)
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      o[e] = (uint32_t)f32_to_bf16_any(v[2 * e] * inv) | ((uint32_t)f32_to_bf16_any(v[2 * e + 1] * inv) << 16);
+    *reinterpret_cast<uint4*>(kv4_chunk(q_smem, row, c / 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(kv4_chunk(q_smem, row, c / 8 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+  __syncwarp();
+  bf16_t* to = real ? p.out + tok * p.o_tok + h * p.o_head : nullptr;
 #pragma unroll 2
-    for (int i = 0; i < CHUNKS; ++i) {
-      const int u = 32 * i + lane, r = u / CHUNKS, c = u - r * CHUNKS;
-      uint8_t* dst = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
-      if (dst != nullptr)
-        *reinterpret_cast<uint4*>(dst + 16 * c) = *reinterpret_cast<const uint4*>(kv4_chunk(q_smem, row0 + r, c));
-    }
-    __syncwarp();
+  for (int i = 0; i < CHUNKS; ++i) {
+    const int u = 32 * i + lane, r = u / CHUNKS, c = u - r * CHUNKS;
+    bf16_t* dst = reinterpret_cast<bf16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
+    if (dst != nullptr)
+      *reinterpret_cast<uint4*>(dst + 8 * c) = *reinterpret_cast<const uint4*>(kv4_chunk(q_smem, row0 + r, c));
   }
+  __syncwarp();
 }
 
-// Grid (row tiles, n_splits, Hkv * B); the last query tiles, which see the most keys when
-// causal, come first.
+// Grid: any number of blocks; Kv4Walk says what each does.
 template <int HD>
 __global__ void __launch_bounds__(AttnKv4TcCfg<HD>::THREADS, 1)
 attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
@@ -309,34 +440,17 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
   uint64_t* q_full = pv_done + 2;    // [2]: tile t's Q is in shared memory
   uint64_t* drain = q_full + 2;      // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
-  volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [0] abort, [1] a page that is none
-
-  pdl_wait();
-  const int sp = blockIdx.y, g = blockIdx.z % p.c.Hkv, b = blockIdx.z / p.c.Hkv;
-  const int tile = gridDim.x - 1 - blockIdx.x;
-  const Kv4Req rq = kv4_request(p, b);
-  const int n_rows = rq.n * p.group, R0 = 256 * tile;
-  if (rq.skip) return;
-  if (rq.bad) {
-    if (tile == 0 && sp == 0) kv4_poison(p, rq, g * p.group, p.group, HD);
-    return;
-  }
-  if (R0 >= n_rows) return;
-  const int nt = n_rows - R0 > 128 ? 2 : 1;
-  const int last = min(n_rows, R0 + 256) - 1;
-  const int ks = sp * p.chunk;
-  const int ke = min(kv4_row_limit(p, rq, last / p.group), ks + p.chunk);
-  const int nblk = ke > ks ? (ke - ks + BK - 1) / BK : 0;
+  volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [0] abort
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < KST; ++s) {
       mbar_init(&k_full[s], G::UNPACK);
-      mbar_init(&k_empty[s], nt);
+      mbar_init(&k_empty[s], 2);
     }
     for (int s = 0; s < VST; ++s) {
       mbar_init(&v_full[s], G::UNPACK);
-      mbar_init(&v_empty[s], nt);
+      mbar_init(&v_empty[s], 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
@@ -346,7 +460,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
       mbar_init(&q_full[t], 4);
       mbar_init(&drain[t], 1);
     }
-    flags[0] = flags[1] = 0;
+    flags[0] = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -354,6 +468,11 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     tmem_alloc(tmem_slot, G::kTmemCols);
     tmem_relinquish();
   }
+  pdl_wait();
+  Kv4Walk<HD> walk;
+  walk.begin(p, reinterpret_cast<long*>(smem));
+  if (p.cut && threadIdx.x < 2) p.parts[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
+  Kv4Work w;
   // Barriers and TMEM are there; the unpacking warps' first page ids are already on their way.
   auto join = [&]() {
     tc_fence_before();
@@ -364,22 +483,24 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
 
   if (warp < 2) {
     join();
-    if (warp < nt) {
-      // ---------------- MMA issuer of tile `warp`: the warp waits as one, an elected lane issues
-      const int t = __shfl_sync(0xffffffffu, warp, 0);
-      const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-      const uint32_t s_col = tm + t * BK, p_col = tm + G::kPCol + t * (BK / 2), o_col = tm + G::kOCol + t * HD;
-      const uint64_t qd = sdesc_k_sw128(smem_u32(smem + t * G::kQTile));
-      const uint64_t kd0 = sdesc_k_sw128(smem_u32(sK)), vd0 = sdesc_mn_sw128(smem_u32(sV), G::kAtom);
-      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, flags));
-      };
-      int kst = 0, vst = 0;        // stages and their parities
-      uint32_t kph = 0, vph = 0;
-      auto issue_s = [&]() -> bool {
-        if (!wait(&k_full[kst], kph)) return false;
-        tc_fence_after();
-        if (elect_one()) {
+    // ---------------- MMA issuer of tile `warp`: the warp waits as one, an elected lane issues
+    const int t = __shfl_sync(0xffffffffu, warp, 0);
+    const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    const uint32_t s_col = tm + t * BK, p_col = tm + G::kPCol + t * (BK / 2), o_col = tm + G::kOCol + t * HD;
+    const uint64_t qd = sdesc_k_sw128(smem_u32(smem + t * G::kQTile));
+    const uint64_t kd0 = sdesc_k_sw128(smem_u32(sK)), vd0 = sdesc_mn_sw128(smem_u32(sV), G::kAtom);
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, flags));
+    };
+    int kst = 0, vst = 0;        // stages and their parities
+    uint32_t kph = 0, vph = 0;
+    uint32_t done = 0, loads = 0;
+    bool live = true;            // the work has rows in this tile; otherwise the stages are only passed on
+    auto issue_s = [&]() -> bool {
+      if (!wait(&k_full[kst], kph)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        if (live) {
           const uint64_t kd = kd0 + kst * (G::kKV >> 4);   // descriptors count 16-byte units
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k)
@@ -387,43 +508,62 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
                       kd + (((k >> 2) * G::kAtom + (k & 3) * 32) >> 4), kIdQK, k != 0);
           umma_commit(&s_full[t]);
           umma_commit(&k_empty[kst]);
+        } else {
+          mbar_arrive(&k_empty[kst]);
         }
-        __syncwarp();
-        if (++kst == KST) { kst = 0; kph ^= 1; }
-        return true;
-      };
-      bool ok = nblk == 0 || (wait(&q_full[t], 0) && issue_s());
+      }
+      __syncwarp();
+      if (++kst == KST) { kst = 0; kph ^= 1; }
+      return true;
+    };
+    bool ok = true;
+    while (ok && walk.next(p, w)) {
+      const int nblk = w.j1 - w.j0;
+      live = t == 0 || w.rq.n * p.group - 256 * w.tile > 128;
+      if (nblk == 0) {
+        if (live && !w.rq.bad) ++loads;
+        continue;
+      }
+      ok = (!live || wait(&q_full[t], loads & 1)) && issue_s();
 #pragma unroll 1
       for (int j = 0; j < nblk && ok; ++j) {
-        if (j + 1 < nblk && !(wait(&s_read[t], j & 1) && issue_s())) { ok = false; break; }
-        if (!wait(&v_full[vst], vph) || !wait(&p_full[t], j & 1)) { ok = false; break; }
+        if (j + 1 < nblk && !((!live || wait(&s_read[t], (done + j) & 1)) && issue_s())) { ok = false; break; }
+        if (!wait(&v_full[vst], vph) || (live && !wait(&p_full[t], (done + j) & 1))) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t vd = vd0 + vst * (G::kKV >> 4);
+          if (live) {
+            const uint64_t vd = vd0 + vst * (G::kKV >> 4);
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            umma_bf16_ts(o_col, p_col + k * 8, vd + ((k * 16 * 128) >> 4), kIdPV, (j | k) != 0);
-          umma_commit(&pv_done[t]);
-          umma_commit(&v_empty[vst]);
+            for (int k = 0; k < BK / 16; ++k)
+              umma_bf16_ts(o_col, p_col + k * 8, vd + ((k * 16 * 128) >> 4), kIdPV, (j | k) != 0);
+            umma_commit(&pv_done[t]);
+            umma_commit(&v_empty[vst]);
+          } else {
+            mbar_arrive(&v_empty[vst]);
+          }
         }
         __syncwarp();
         if (++vst == VST) { vst = 0; vph ^= 1; }
       }
-      if (!ok) flags[0] = 1;
-      if (elect_one()) umma_commit(&drain[t]);
-      __syncwarp();
-      mbar_drain(&drain[t], 0);
-      __syncwarp();
+      if (live) {
+        done += nblk;
+        ++loads;
+      }
     }
+    if (!ok) flags[0] = 1;
+    if (elect_one()) umma_commit(&drain[t]);
+    __syncwarp();
+    mbar_drain(&drain[t], 0);
+    __syncwarp();
   } else if (warp >= 10) {
     // ---------------- unpacking: GPW times 8 keys of each block, lane / 4 the key, lane % 4 the group of an atom
     constexpr int GPW = G::GPW;
     const int k8 = lane >> 2, grp = lane & 3;
     const int key0 = 8 * (warp - 10) + k8;                      // and key0 + 48
-    const int* trow = p.table + (long)b * p.stride;
     const int mask = (1 << p.c.page_shift) - 1;
     const long v_rows = (long)p.c.Hkv << p.c.page_shift, page_rows = 2 * v_rows;
-    const int head_row = g << p.c.page_shift;
+    const int* trow = nullptr;
+    int head_row = 0, ks = 0, ke = 0, nblk = 0;
     uint2 code[2][GPW][AT];
     uint32_t byte[2][GPW][AT];
     int id_k[GPW], id_v[GPW];
@@ -438,14 +578,11 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     // an entry that is no page becomes -1
     auto check = [&](int (&id)[GPW]) {
 #pragma unroll
-      for (int i = 0; i < GPW; ++i) {
-        if (id[i] != -2 && (id[i] < 0 || id[i] >= p.c.n_pages)) {
-          id[i] = -1;
-          flags[1] = 1;
-        }
-      }
+      for (int i = 0; i < GPW; ++i)
+        if (id[i] != -2 && (id[i] < 0 || id[i] >= p.c.n_pages)) id[i] = -1;
     };
-    // a block's bytes of K or V; a key that does not exist has scale 0 and becomes 0
+    // a block's bytes of K or V; a key that does not exist has scale 0 and becomes 0; one in no page has an
+    // infinite scale in K, which makes it NaN (infinity - infinity), and with it the rows that see it
     auto fetch = [&](int kv, int j, const int (&id)[GPW]) {
 #pragma unroll
       for (int i = 0; i < GPW; ++i) {
@@ -455,7 +592,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
 #pragma unroll
         for (int a = 0; a < AT; ++a) {
           code[kv][i][a] = make_uint2(0, 0);
-          byte[kv][i][a] = 0;
+          byte[kv][i][a] = kv == 0 && id[i] == -1 ? 0x7F8 : 0;
           if (id[i] >= 0 && 16 * (4 * a + grp) < HD) {
             code[kv][i][a] = *reinterpret_cast<const uint2*>(pc + 32 * a);
             byte[kv][i][a] = ps[4 * a];
@@ -466,86 +603,108 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     const uint32_t at0 = key0 * 128 + (((2 * grp) ^ k8) << 4);
     const Kv4Masks masks{p.mask_low, p.mask_high};
     bool ok = true;
-    // K runs a block ahead of V, as S runs ahead of P V: the turns are K(0), K(1), V(0), K(2), V(1), ...
-    ask(0, id_v);
-    ask(1, id_k);
-    join();
-    check(id_v);
-    fetch(0, 0, id_v);
-    fetch(1, 0, id_v);
+    // the next work's first page ids
+    auto open = [&]() -> bool {
+      do {
+        if (!walk.next(p, w)) return false;
+      } while (w.j1 == w.j0);
+      nblk = w.j1 - w.j0;
+      ks = w.j0 * BK;
+      ke = min(w.j1 * BK, kv4_row_limit(p, w.rq, (min(w.rq.n * p.group, 256 * (w.tile + 1)) - 1) / p.group));
+      trow = p.table + (long)w.b * p.stride;
+      head_row = w.h << p.c.page_shift;
+      ask(0, id_v);
+      ask(1, id_k);
+      return true;
+    };
     int kst = 0, vst = 0;            // stages, and the parities of their being empty
     uint32_t kph = 1, vph = 1;
+    bool more = open();
+    join();
+    while (more) {
+      // K runs a block ahead of V, as S runs ahead of P V: the turns are K(0), K(1), V(0), K(2), V(1), ...
+      check(id_v);
+      fetch(0, 0, id_v);
+      fetch(1, 0, id_v);
 #pragma unroll 1
-    for (int j = -1; j < nblk && ok; ++j) {
-      // this turn's bytes have had a block's time to arrive; all loads of the next one are issued
-      // together before any is waited for again
-      uint2 now[2][GPW][AT];
-      uint32_t scale[2][GPW][AT];
+      for (int j = -1; j < nblk && ok; ++j) {
+        // this turn's bytes have had a block's time to arrive; all loads of the next one are issued
+        // together before any is waited for again
+        uint2 now[2][GPW][AT];
+        uint32_t scale[2][GPW][AT];
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv)
+        for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
-        for (int i = 0; i < GPW; ++i)
+          for (int i = 0; i < GPW; ++i)
 #pragma unroll
-          for (int a = 0; a < AT; ++a) {
-            if (kv == 1 && j < 0) continue;
-            now[kv][i][a] = code[kv][i][a];
-            scale[kv][i][a] = byte[kv][i][a];
-            asm volatile("" : "+r"(now[kv][i][a].x), "+r"(now[kv][i][a].y), "+r"(scale[kv][i][a]));
-          }
-      check(id_k);
-      fetch(0, j + 2, id_k);
-      if (j >= 0) fetch(1, j + 1, id_v);
-#pragma unroll
-      for (int i = 0; i < GPW; ++i) id_v[i] = id_k[i];
-      ask(j + 3, id_k);
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int jb = kv ? j : j + 1;
-        if (jb < 0 || jb >= nblk) continue;
-        const int st = kv ? vst : kst;
-        if (!__all_sync(0xffffffffu, mbar_wait(&(kv ? v_empty : k_empty)[st], kv ? vph : kph, flags))) {
-          ok = false;
-          break;
-        }
-        if (kv == 0 && ++kst == KST) { kst = 0; kph ^= 1; }
-        if (kv == 1 && ++vst == VST) { vst = 0; vph ^= 1; }
-        uint8_t* dst = (kv ? sV : sK) + st * G::kKV + at0;
-        uint8_t* dst2 = (kv ? sV : sK) + st * G::kKV + (at0 ^ 16);
-#pragma unroll
-        for (int i = 0; i < GPW; ++i)
-#pragma unroll
-          for (int a = 0; a < AT; ++a) {
-            if (16 * (4 * a + grp) < HD) {
-              uint32_t o[8];
-              if (kv == 0) {
-                const __nv_bfloat162 sc = kv4_scale_bf16x2(scale[kv][i][a]);
-                const __nv_bfloat162 m24 = __hmul2(sc, __float2bfloat162_rn(-24.f));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  o[e] = kv4_bf16x2_masked(now[kv][i][a].x, e, sc, m24, p.mask_bf16);
-                  o[4 + e] = kv4_bf16x2_masked(now[kv][i][a].y, e, sc, m24, p.mask_bf16);
-                }
-              } else {
-                const Kv4Scale2 sc = kv4_scale2(scale[kv][i][a] * 0x00800080u);
-                kv4_sixteenth(now[kv][i][a].x, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[0]));
-                kv4_sixteenth(now[kv][i][a].y, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[4]));
-              }
-              *reinterpret_cast<uint4*>(dst + a * G::kAtom + i * 48 * 128) = make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4*>(dst2 + a * G::kAtom + i * 48 * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+            for (int a = 0; a < AT; ++a) {
+              if (kv == 1 && j < 0) continue;
+              now[kv][i][a] = code[kv][i][a];
+              scale[kv][i][a] = byte[kv][i][a];
+              asm volatile("" : "+r"(now[kv][i][a].x), "+r"(now[kv][i][a].y), "+r"(scale[kv][i][a]));
             }
+        check(id_k);
+        fetch(0, j + 2, id_k);
+        if (j >= 0) fetch(1, j + 1, id_v);
+#pragma unroll
+        for (int i = 0; i < GPW; ++i) id_v[i] = id_k[i];
+        ask(j + 3, id_k);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int jb = kv ? j : j + 1;
+          if (jb < 0 || jb >= nblk) continue;
+          const int st = kv ? vst : kst;
+          if (!__all_sync(0xffffffffu, mbar_wait(&(kv ? v_empty : k_empty)[st], kv ? vph : kph, flags))) {
+            ok = false;
+            break;
           }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&(kv ? v_full : k_full)[st]);
+          if (kv == 0 && ++kst == KST) { kst = 0; kph ^= 1; }
+          if (kv == 1 && ++vst == VST) { vst = 0; vph ^= 1; }
+          uint8_t* dst = (kv ? sV : sK) + st * G::kKV + at0;
+          uint8_t* dst2 = (kv ? sV : sK) + st * G::kKV + (at0 ^ 16);
+#pragma unroll
+          for (int i = 0; i < GPW; ++i)
+#pragma unroll
+            for (int a = 0; a < AT; ++a) {
+              if (16 * (4 * a + grp) < HD) {
+                uint32_t o[8];
+                if (kv == 0) {
+                  const __nv_bfloat162 sc = kv4_scale_bf16x2(scale[kv][i][a]);
+                  const __nv_bfloat162 m24 = __hmul2(sc, __float2bfloat162_rn(-24.f));
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    o[e] = kv4_bf16x2_masked(now[kv][i][a].x, e, sc, m24, p.mask_bf16);
+                    o[4 + e] = kv4_bf16x2_masked(now[kv][i][a].y, e, sc, m24, p.mask_bf16);
+                  }
+                } else {
+                  const Kv4Scale2 sc = kv4_scale2(scale[kv][i][a] * 0x00800080u);
+                  kv4_sixteenth(now[kv][i][a].x, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[0]));
+                  kv4_sixteenth(now[kv][i][a].y, sc, masks, reinterpret_cast<uint32_t(&)[4]>(o[4]));
+                }
+                *reinterpret_cast<uint4*>(dst + a * G::kAtom + i * 48 * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(dst2 + a * G::kAtom + i * 48 * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+              }
+            }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&(kv ? v_full : k_full)[st]);
+        }
       }
+      more = ok && open();
     }
     if (!ok) flags[0] = 1;
   } else {
     join();
     const int t = (warp - 2) >> 2;
-    if (t < nt)
-      kv4_softmax_tile<HD>(p, rq, tmem_slot, s_full, s_read, p_full, pv_done, q_full, smem + t * G::kQTile, flags, t, R0, g, sp,
-                           ks, ke, nblk);
+    uint32_t done = 0;
+    while (walk.next(p, w)) {
+      if (w.rq.bad) {
+        if (t == 0) kv4_poison(p, w.rq, w.h * p.group, p.group, HD, threadIdx.x - 64, 128);
+      } else if (t == 0 || w.rq.n * p.group - 256 * w.tile > 128) {
+        kv4_softmax_tile<HD>(p, w, tmem_slot, s_full, s_read, p_full, pv_done, q_full, smem + t * G::kQTile, flags, t, done);
+        done += w.j1 - w.j0;
+      }
+    }
   }
   __syncwarp();
   tc_fence_before();
@@ -554,6 +713,95 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
   if (warp == 0) {
     __syncwarp();
     tmem_dealloc(*tmem_slot, G::kTmemCols);
+  }
+}
+
+constexpr int kKv4MaxBlocks = 160;   // of attn_kv4_tc_kernel: what attn_kv4_parts_kernel has room for
+
+// Joins the parts of tiles that several of `blocks` blocks shared. One wave of blocks (256 threads each),
+// which look up which tiles there are and deal out pieces of 8 dims of one, a row per thread. What
+// bounds it is the latency of loads that depend on one another, so a thread has up to four parts' loads
+// under way. (A block per tile and piece, most of which ended at once: as long as the joins.)
+template <int HD>
+__global__ void __launch_bounds__(256, 4)
+attn_kv4_parts_kernel(const __grid_constant__ AttnKv4Params p, int blocks) {
+  constexpr int PIECES = HD / 8, WORDS = kKv4MaxBlocks / 32, K = 4;
+  __shared__ unsigned begun[WORDS], ended[WORDS];   // a bit per block: it began a tile that goes on, it ended one
+  __shared__ int4 tile[kKv4MaxBlocks];              // (request, KV head, tile, first block and number of blocks << 16)
+  pdl_begin();
+  const int row = threadIdx.x, lane = row & 31;
+  int4 what = make_int4(0, 0, 0, 0);
+  if (row < kKv4MaxBlocks) {
+    int end = 0;
+    if (row < blocks) {
+      what = p.parts[2 * row + 1];
+      end = p.parts[2 * row].w;
+    }
+    const unsigned x = __ballot_sync(0xffffffffu, what.w != 0), y = __ballot_sync(0xffffffffu, end == 2);
+    if (lane == 0) {
+      begun[row >> 5] = x;
+      ended[row >> 5] = y;
+    }
+  }
+  __syncthreads();
+  int tiles = 0, before = 0;
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) {
+    const unsigned x = begun[i];
+    tiles += __popc(x);
+    if (32 * i < row) before += __popc(row - 32 * i < 32 ? x & ((1u << (row - 32 * i)) - 1) : x);
+  }
+  if (what.w != 0) {   // the block that ends the tile: the next one that ends any
+    int j = (row + 1) >> 5;
+    unsigned rest = j < WORDS ? ended[j] & (0xffffffffu << ((row + 1) & 31)) : 0;
+    while (rest == 0 && j < WORDS - 1) rest = ended[++j];
+    tile[before] = make_int4(what.x, what.y, what.z, row | (rest == 0 ? 1 : 32 * j + __ffs(rest) - row) << 16);
+  }
+  __syncthreads();
+  for (int item = blockIdx.x; item < tiles * PIECES; item += gridDim.x) {
+    const int piece = item % PIECES;
+    what = tile[item / PIECES];
+    const int first = what.w & 0xFFFF, n = what.w >> 16;
+    const float4* o = reinterpret_cast<const float4*>(p.part_o) + 2 * piece * 256 + row;
+    const Kv4Req rq = kv4_request(p, what.x);
+    float mx = -INFINITY, all = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    for (int s = 0; s < n; s += K) {
+      float lse[K];
+      float4 x[K], y[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (s + k >= n) continue;
+        const long part = 2 * (first + s + k) + (s + k == 0);
+        lse[k] = p.part_lse[part * 256 + row];
+        x[k] = o[part * 64 * HD];
+        y[k] = o[part * 64 * HD + 256];
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (s + k >= n) continue;
+        const float top = fmaxf(mx, lse[k]);
+        const float base = top == -INFINITY ? 0.f : top;
+        const float f = exp2f(mx - base), w = exp2f(lse[k] - base);   // a part with NaN makes all NaN
+        mx = top;
+        all = all * f + w;
+        a = make_float4(a.x * f + w * x[k].x, a.y * f + w * x[k].y, a.z * f + w * x[k].z, a.w * f + w * x[k].w);
+        b = make_float4(b.x * f + w * y[k].x, b.y * f + w * y[k].y, b.z * f + w * y[k].z, b.w * f + w * y[k].w);
+      }
+    }
+    const int R = 256 * what.z + row;
+    if (R >= rq.n * p.group) continue;
+    const long t = rq.q0 + R / p.group;
+    const int h = what.y * p.group + R % p.group;
+    const float inv = all == 0.f ? 0.f : 1.f / all;
+    uint4 out;
+    out.x = (uint32_t)f32_to_bf16_any(a.x * inv) | ((uint32_t)f32_to_bf16_any(a.y * inv) << 16);
+    out.y = (uint32_t)f32_to_bf16_any(a.z * inv) | ((uint32_t)f32_to_bf16_any(a.w * inv) << 16);
+    out.z = (uint32_t)f32_to_bf16_any(b.x * inv) | ((uint32_t)f32_to_bf16_any(b.y * inv) << 16);
+    out.w = (uint32_t)f32_to_bf16_any(b.z * inv) | ((uint32_t)f32_to_bf16_any(b.w * inv) << 16);
+    *reinterpret_cast<uint4*>(p.out + t * p.o_tok + h * p.o_head + 8 * piece) = out;
+    if (piece == 0 && p.lse != nullptr)
+      p.lse[t * p.H + h] = all == 0.f ? -INFINITY : (mx + log2f(all)) * 0.6931471805599453f;
   }
 }
 

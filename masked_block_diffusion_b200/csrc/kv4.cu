@@ -22,6 +22,7 @@ cudaError_t kv4_set_wait_limit(unsigned long long ns) { return cudaMemcpyToSymbo
 namespace {
 
 constexpr int kSMs = 148;
+static_assert(kSMs <= kKv4MaxBlocks, "attn_kv4_parts_kernel");
 
 int ceil_div(long a, long b) { return (int)((a + b - 1) / b); }
 
@@ -109,39 +110,38 @@ bool addr_ok(const int32_t* req, const int32_t* pos, const int32_t* table, int n
 
 struct AttnPlan {
   int tiles, n_splits, chunk;
-  int nr;   // 8-row columns of the few-row kernel; 0: the tensor-core kernel
+  int nr;    // 8-row columns of the few-row kernel; 0: the tensor-core kernel
+  bool cut;  // which may cut tiles into parts
 };
 
-// Query rows per block: 8 or 16 of the few-row kernel, else 256 of the tensor-core kernel.
-AttnPlan attn_plan(int B, int max_q, int max_kv, int group, int Hkv, int hd) {
-  AttnPlan a;
+// Up to 16 rows per KV head and request: the few-row kernel, 8 or 16 rows and a split of the keys per
+// block. More: the tensor-core kernel, which deals its work out by itself.
+AttnPlan attn_plan(int B, int max_q, int max_kv, int group, int Hkv) {
+  AttnPlan a{0, 1, 0, 0, max_kv > 512};
   const long rows = (long)max_q * group;
   a.nr = rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
-  a.tiles = ceil_div(rows, a.nr ? 8 * a.nr : 256);
+  if (a.nr == 0) return a;
+  a.tiles = ceil_div(rows, 8 * a.nr);
   // Blocks that the GPU holds at a time, and blocks without a split.
-  const long slots = kSMs * (a.nr == 1 ? 4 : a.nr == 2 ? 2 : 1);
+  const long slots = kSMs * (a.nr == 1 ? 4 : 2);
   const long blocks = (long)B * Hkv * a.tiles;
   long want;
-  if (a.nr == 0) {
-    // As many as still run at once. 256 queries over 2048 keys (16 blocks): 1 split 106 us, 2 64, 4 42, 8 31, 9 (this
-    // rule) 30, 12 47. Two splits of calls that fill the GPU are no faster: 16 such canvases 184 -> 244 us, and three
-    // prompt pieces, the longest of 1024 queries over 4096 keys, 125 -> 124.
-    want = slots / blocks;
-  } else if (blocks * ceil_div(max_kv, 256) <= slots) {
+  if (blocks * ceil_div(max_kv, 256) <= slots) {
     want = ceil_div(max_kv, 256);                      // a short call: as wide as it goes
   } else {
     // one wave of blocks when a few requests share the GPU; else blocks of 512 keys or more and
     // about two waves of them, so that requests of different lengths even out
     want = blocks >= slots / 4 ? std::min<long>(ceil_div(2 * slots, blocks), ceil_div(max_kv, 512)) : slots / blocks;
   }
-  want = std::max(1L, std::min<long>(want, ceil_div(max_kv, a.nr ? 64 : 128)));
-  const int grain = a.nr ? 128 : hd == 64 ? 96 : 48;   // keys of a kernel's stage or block
+  want = std::max(1L, std::min<long>(want, ceil_div(max_kv, 64)));
+  const int grain = 128;   // keys of a stage
   a.chunk = std::max(grain, ceil_div(ceil_div(max_kv, want), grain) * grain);
   a.n_splits = std::max(1, ceil_div(max_kv, a.chunk));
   return a;
 }
 
 size_t attn_workspace(const AttnPlan& a, int T, int H, int hd) {
+  if (a.nr == 0) return !a.cut ? 0 : (size_t)kSMs * 2 * (256 * (hd + 1) * sizeof(float) + sizeof(int4));
   if (a.n_splits == 1) return 0;
   return (size_t)a.n_splits * T * H * (hd + 1) * sizeof(float);
 }
@@ -169,18 +169,15 @@ cudaError_t run_tc(cudaStream_t st, const AttnPlan& a, const AttnKv4Params& p) {
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(attn_kv4_tc_kernel<HD>),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, G::kTotal);
   if (e != cudaSuccess) return e;
-  return launch(st, attn_kv4_tc_kernel<HD>, dim3(a.tiles, a.n_splits, p.c.Hkv * p.B), G::THREADS, G::kTotal, p);
+  return launch(st, attn_kv4_tc_kernel<HD>, dim3(kSMs), G::THREADS, G::kTotal, p);
 }
 
 template <int HD>
 cudaError_t run_attn(cudaStream_t st, const AttnPlan& a, const AttnKv4Params& p) {
   cudaError_t e = a.nr == 1 ? run_few<HD, 1>(st, a, p) : a.nr == 2 ? run_few<HD, 2>(st, a, p) : run_tc<HD>(st, a, p);
-  if (e == cudaSuccess && a.n_splits > 1)
-    // Many rows: a warp per row (256 queries of 16 heads in 9 splits: 33.3 us with a block per row, 30.4 with a
-    // warp). A few: a block per row, whose warps share the splits (16 rows in 17 splits: 12.1 us, 13.6 with a warp).
-    e = a.nr == 0 && a.n_splits <= 32
-            ? launch(st, attn_kv4_merge_rows_kernel<HD>, dim3(ceil_div((long)p.max_q * p.H, 8), p.B), 256, 0, p)
-            : launch(st, attn_kv4_merge_kernel<HD>, dim3((unsigned)p.max_q * p.H, p.B), 128, 0, p);
+  if (e != cudaSuccess) return e;
+  if (a.nr == 0) return !a.cut ? e : launch(st, attn_kv4_parts_kernel<HD>, dim3(4 * kSMs), 256, 0, p, kSMs);
+  if (a.n_splits > 1) e = launch(st, attn_kv4_merge_kernel<HD>, dim3((unsigned)p.max_q * p.H, p.B), 128, 0, p);
   return e;
 }
 
@@ -312,7 +309,7 @@ int dllm_op_read_kv4(const dllm_kv4* cache, const int32_t* req, const int32_t* p
 long long dllm_op_attn_kv4_workspace(const dllm_kv4* cache, int B, int T, int max_q, int max_kv, int H) {
   if (!cache_ok(cache) || !attn_sizes_ok(cache, B, T, max_q, max_kv, H)) return DLLM_E_INVAL;
   if (B == 0 || max_q == 0) return 0;
-  const AttnPlan a = attn_plan(B, max_q, max_kv, H / cache->n_kv_heads, cache->n_kv_heads, cache->head_dim);
+  const AttnPlan a = attn_plan(B, max_q, max_kv, H / cache->n_kv_heads, cache->n_kv_heads);
   return (long long)attn_workspace(a, T, H, cache->head_dim);
 }
 
@@ -329,9 +326,8 @@ int dllm_op_attn_kv4(const dllm_kv4* cache, const uint16_t* q, long long q_token
       !vectors(out, DLLM_BF16, out_token_stride, out_head_stride) || !aligned16(workspace))
     return DLLM_E_INVAL;
   const int group = H / cache->n_kv_heads;
-  const AttnPlan a = attn_plan(B, max_q, max_kv, group, cache->n_kv_heads, cache->head_dim);
-  if ((a.nr ? (long)cache->n_kv_heads * a.tiles : (long)cache->n_kv_heads * B) > 65535 || a.n_splits > 65535)
-    return DLLM_E_INVAL;
+  const AttnPlan a = attn_plan(B, max_q, max_kv, group, cache->n_kv_heads);
+  if ((long)cache->n_kv_heads * a.tiles > 65535) return DLLM_E_INVAL;   // the few-row kernel's grid
   if (attn_workspace(a, T, H, cache->head_dim) > (workspace ? workspace_bytes : 0)) return DLLM_E_INVAL;
   AttnKv4Params p;
   p.c = cache_of(cache);
@@ -360,7 +356,10 @@ int dllm_op_attn_kv4(const dllm_kv4* cache, const uint16_t* q, long long q_token
   p.mask_high = 0x03C003C0u;
   p.mask_bf16 = 0x00780078u;
   p.part_o = reinterpret_cast<float*>(workspace);
-  p.part_lse = p.part_o + (size_t)a.n_splits * T * H * cache->head_dim;
+  const size_t part_rows = a.nr == 0 ? (size_t)kSMs * 512 : (size_t)a.n_splits * T * H;
+  p.part_lse = p.part_o + part_rows * cache->head_dim;
+  p.cut = a.cut;
+  p.parts = reinterpret_cast<int4*>(p.part_lse + part_rows);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = cache->head_dim == 176   ? run_attn<176>(st, a, p)
                         : cache->head_dim == 128 ? run_attn<128>(st, a, p)

@@ -393,6 +393,51 @@ def test_attention_of_one_tile_in_many_splits(d, keys):
     attend_case(d, 2, 1, 64, [20], [keys], True, seed=22)
 
 
+@pytest.mark.parametrize("d,h,hk", [(64, 8, 2), (128, 2, 2), (176, 4, 2)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_of_many_tiles_in_equal_shares(d, h, hk, causal):
+    """Tiles that start and end anywhere in a block's share: ragged requests, some without queries or keys."""
+    rng = np.random.default_rng(d + causal)
+    queries = [int(n) for n in rng.integers(0, 150, 40)]
+    keys = [int(n) for n in rng.integers(0, 700, 40)]
+    queries[:6], keys[:6] = [150, 0, 130, 64, 129, 1], [700, 300, 0, 64, 96, 1]
+    queries[-3:], keys[-3:] = [140, 0, 0], [0, 5, 0]
+    attend_case(d, h, hk, 32, queries, keys, causal, seed=25)
+
+
+@pytest.mark.parametrize("d,keys,n", [(64, 9000, 1), (176, 5000, 2), (128, 40, 1)])
+def test_attention_of_one_tile_among_many_empty_requests(d, keys, n):
+    """The batch is sized for more requests than there are: one tile's keys over all blocks, or a block per tile."""
+    B = 90
+    queries, lens = [0] * B, [0] * B
+    for i in range(n):
+        queries[60 * i + 5], lens[60 * i + 5] = 20, keys - 700 * i
+    attend_case(d, 2, 1, 64, queries, lens, True, seed=26)
+
+
+def test_attention_of_many_tiles_answers_bad_requests_with_nan():
+    rng = np.random.default_rng(27)
+    B, queries, keys, page, h, hk, d = 40, 70, 300, 32, 4, 2, 64
+    cache, table, held = filled(rng, [keys] * B, page, hk, d)
+    q = torch.tensor(rng.normal(size=(B * queries, h, d)), device="cuda").bfloat16()
+    starts = np.arange(B + 1) * queries
+    lens = np.full(B, keys)
+    lens[[0, 7, 39]] = [-1, keys + page + 5, keys + 1000]
+    table[12, 3] = cache.n_pages
+    table[30, (keys - 1) // page] = -1
+    out, lse = cache.attend(q, i32(starts), i32(lens), i32(table), max_q=queries, max_kv=keys + 500, causal=True, return_lse=True)
+    for b in range(B):
+        rows = slice(b * queries, (b + 1) * queries)
+        if b in (0, 7, 39):
+            assert torch.isnan(out[rows]).all() and torch.isnan(lse[rows]).all(), b
+        elif b in (12, 30):                                           # the rows that see the page
+            lost = torch.isnan(lse[rows]).all(-1).cpu().numpy()
+            assert lost[np.arange(queries) + keys - queries >= 32 * (3 if b == 12 else (keys - 1) // page)].all()
+            assert torch.equal(torch.isnan(out[rows]).all(-1), torch.isnan(lse[rows]))
+        else:
+            check_attention(out[rows], lse[rows], q[rows], [held[b]], [queries], [keys], True, d ** -0.5)
+
+
 @pytest.mark.parametrize("queries", [1, 30])
 def test_attention_without_a_key_and_in_place(queries):
     cache, table, held = filled(np.random.default_rng(23), [70], 16, 2, 64)
