@@ -54,6 +54,7 @@ struct AttnKv4Params {
   // parts[i] = (request, KV head, tile, 1: goes on in the next block, 2: ends here; 0: no such part)
   int4* parts;
   int cut;                  // 0: tiles stay whole, and there are no parts
+  int unit_shift;           // Kv4Walk
   uint32_t mask_low, mask_high;   // Kv4Masks
   uint32_t mask_bf16;             // 0x00780078
 };

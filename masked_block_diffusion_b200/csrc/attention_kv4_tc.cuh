@@ -67,7 +67,8 @@ struct AttnKv4TcCfg {
   static constexpr int kOffK = 2 * kQTile;
   static constexpr int kOffV = kOffK + KST * kKV;
   static constexpr int kOffBar = kOffV + VST * kKV;
-  static constexpr int kTotal = kOffBar + 256 + 1024;
+  static constexpr int kOffShare = kOffBar + 256;        // Kv4Walk::begin's
+  static constexpr int kTotal = kOffShare + 256 + 1024;
   static constexpr int kPCol = 2 * BK;
   static constexpr int kOCol = 3 * BK;
   static constexpr int kTmemCols = 512;
@@ -103,6 +104,11 @@ DLLM_DEV uint32_t kv4_bf16x2_masked(uint32_t w, int j, __nv_bfloat162 s, __nv_bf
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+DLLM_DEV uint32_t kv4_bf16_pair(float lo, float hi) {   // to nearest even, NaN stays one
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // 16 bytes from global to shared memory, `n` of them (0 or 16) read and the others 0.
 DLLM_DEV void copy16(void* dst, const void* src, int n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
@@ -114,9 +120,6 @@ DLLM_DEV void copy16(void* dst, const void* src, int n) {
 DLLM_DEV uint8_t* kv4_chunk(uint8_t* tile, int r, int c) {
   return tile + (c >> 3) * 128 * 128 + r * 128 + (((c ^ r) & 7) << 4);
 }
-
-// a / b for a >= 0, b > 0: in 32 bits where they fit, since every thread does it and 64 bits take ten times as long.
-DLLM_DEV long kv4_div(long a, long b) { return (a | b) >> 32 ? a / b : (long)((uint32_t)a / (uint32_t)b); }
 
 // A row tile over key blocks j0 .. j1 - 1.
 struct Kv4Work {
@@ -135,8 +138,7 @@ template <int HD>
 struct Kv4Walk {
   using G = AttnKv4TcCfg<HD>;
   int b, h, i, x;           // the next tile, and how far into it the share begins
-  long left;
-  int tiles;
+  int left, tiles;
   Kv4Req rq;
 
   DLLM_DEV int blocks(const AttnKv4Params& p, int tile) const {
@@ -149,77 +151,88 @@ struct Kv4Walk {
     rq = kv4_request(p, b);
     tiles = rq.bad ? rq.n > 0 : (rq.n * p.group + 255) / 256;   // a bad request is answered with its first tile
   }
-  DLLM_DEV int cost(const AttnKv4Params& p, int tile) const { return p.cut ? G::START + blocks(p, tile) : 1; }
-  DLLM_DEV long costs(const AttnKv4Params& p) const {
+  // in units of 2^unit_shift key blocks, so that all of a call's fit 32 bits
+  DLLM_DEV int cost(const AttnKv4Params& p, int tile) const {
+    return p.cut ? G::START + ((blocks(p, tile) + (1 << p.unit_shift) - 1) >> p.unit_shift) : 1;
+  }
+  DLLM_DEV int costs(const AttnKv4Params& p) const {
     if (!p.cut) return tiles;
-    long c = 0;
+    int c = 0;
     for (int t = 0; t < tiles; ++t) c += cost(p, t);
     return c;
   }
-  // All threads; mem: 16 bytes and 16 per warp, free again after the next barrier.
-  DLLM_DEV void begin(const AttnKv4Params& p, long* mem) {
-    constexpr int WARPS = G::THREADS / 32;
+  // All threads; mem: MEM ints that stay as they are until the next barrier. Half of the time of a kernel that
+  // has little to do is code that is fetched to run once, so 32 bits, few divisions and one barrier, which
+  // serves as the kernel's too.
+  static constexpr int WARPS = G::THREADS / 32, MEM = 2 * WARPS + 8;
+  DLLM_DEV void begin(const AttnKv4Params& p, int* mem) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int r0 = (int)((long)p.B * tid / G::THREADS), r1 = (int)((long)p.B * (tid + 1) / G::THREADS);
-    long mine = 0, some = 0;
+    const int r0 = p.B * tid / G::THREADS, r1 = p.B * (tid + 1) / G::THREADS;
+    int mine = 0, some = 0;
     for (int r = r0; r < r1; ++r) {
       request(p, r);
       mine += p.c.Hkv * costs(p);
       some += p.c.Hkv * tiles;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) some += __shfl_xor_sync(0xffffffffu, some, o);
-    long upto = mine;
+    some = __reduce_add_sync(0xffffffffu, some);
+    int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long v = __shfl_up_sync(0xffffffffu, upto, o);
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += v;
     }
     if (lane == 31) {
       mem[warp] = upto;
       mem[WARPS + warp] = some;
     }
-    int* found = reinterpret_cast<int*>(mem + 2 * WARPS);
+    int* found = mem + 2 * WARPS;
     __syncthreads();
-    long all = 0, count = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      upto += w < warp ? mem[w] : 0;
-      all += mem[w];
-      count += mem[WARPS + w];
-    }
+    // lane w of every warp adds up the warps before warp w
+    const int sum = lane < WARPS ? mem[lane] : 0;
+    const int count = __reduce_add_sync(0xffffffffu, lane < WARPS ? mem[WARPS + lane] : 0);
+    const int all = __reduce_add_sync(0xffffffffu, sum);
+    upto += __reduce_add_sync(0xffffffffu, lane < warp ? sum : 0);
     // no share is empty but the last blocks', so that a tile's parts lie in consecutive blocks
-    long n = min(all, (long)gridDim.x);
-    if (count > 0 && count < n) n = kv4_div(n, count) * count;
-    const long k = min((long)blockIdx.x, n);
-    const long lo = n > 0 ? kv4_div(all * k, n) : 0;
-    left = k < n ? kv4_div(all * (k + 1), n) - lo : 0;
-    if (lo >= upto - mine && lo < upto) {
-      long rest = lo - (upto - mine);
+    int n = min(all, (int)gridDim.x), lo = 0;
+    left = 0;
+    if (count > 0 && count < n) n = n / count * count;
+    if ((int)blockIdx.x < n) {
+      const int each = all / n, more = all - each * n, k = blockIdx.x;
+      lo = each * k + more * k / n;
+      left = each * (k + 1) + more * (k + 1) / n - lo;
+    }
+    if (left > 0 && lo >= upto - mine && lo < upto) {
+      int rest = lo - (upto - mine);
       for (int r = r0; r < r1; ++r) {
         request(p, r);
-        const long c = costs(p);
+        const int c = costs(p);
         if (rest >= p.c.Hkv * c) {
           rest -= p.c.Hkv * c;
           continue;
         }
         found[0] = r;
-        found[1] = (int)kv4_div(rest, c);
-        rest -= found[1] * c;
+        found[1] = rest / c;
+        rest -= rest / c * c;
         int t = tiles - 1;
         for (int c1 = cost(p, t); rest >= c1; c1 = cost(p, --t)) rest -= c1;
         found[2] = t;
-        found[3] = (int)rest;
+        found[3] = rest;
+        found[4] = tiles;
+        found[5] = rq.q0;
+        found[6] = rq.n;
+        found[7] = rq.bad ? -1 : rq.kv;
         break;
       }
     }
+    tc_fence_before();
     __syncthreads();
-    if (left > 0) {
-      request(p, found[0]);
-      h = found[1];
-      i = found[2];
-      x = found[3];
-    }
+    tc_fence_after();
+    b = found[0];
+    h = found[1];
+    i = found[2];
+    x = found[3];
+    tiles = found[4];
+    rq = Kv4Req{found[5], found[6], found[7], false, found[7] < 0};
   }
   DLLM_DEV bool next(const AttnKv4Params& p, Kv4Work& w) {
     while (left > 0) {
@@ -232,8 +245,9 @@ struct Kv4Walk {
         i = tiles - 1;
         continue;
       }
-      const int all = blocks(p, i), take = (int)min(left, (long)(cost(p, i) - x));
-      const int j0 = p.cut ? max(0, x - G::START) : 0, j1 = p.cut ? max(0, x + take - G::START) : all;
+      const int all = blocks(p, i), take = min(left, cost(p, i) - x);
+      const int j0 = p.cut ? max(0, x - G::START) << p.unit_shift : 0;
+      const int j1 = p.cut ? min(all, max(0, x + take - G::START) << p.unit_shift) : all;
       const bool begun = x == 0;
       w = Kv4Work{b, h, i, j0, j1, j0 == 0, j1 == all, rq};
       left -= take;
@@ -401,7 +415,7 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const u
     uint32_t o[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      o[e] = (uint32_t)f32_to_bf16_any(v[2 * e] * inv) | ((uint32_t)f32_to_bf16_any(v[2 * e + 1] * inv) << 16);
+      o[e] = kv4_bf16_pair(v[2 * e] * inv, v[2 * e + 1] * inv);
     *reinterpret_cast<uint4*>(kv4_chunk(q_smem, row, c / 8)) = make_uint4(o[0], o[1], o[2], o[3]);
     *reinterpret_cast<uint4*>(kv4_chunk(q_smem, row, c / 8 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
   }
@@ -469,20 +483,14 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     tmem_relinquish();
   }
   pdl_wait();
-  Kv4Walk<HD> walk;
-  walk.begin(p, reinterpret_cast<long*>(smem));
   if (p.cut && threadIdx.x < 2) p.parts[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
+  Kv4Walk<HD> walk;
+  static_assert(4 * Kv4Walk<HD>::MEM <= 256, "share");
+  walk.begin(p, reinterpret_cast<int*>(smem + G::kOffShare));   // barriers and TMEM are there after it
+  pdl_trigger();                                                // after the TMEM allocation
   Kv4Work w;
-  // Barriers and TMEM are there; the unpacking warps' first page ids are already on their way.
-  auto join = [&]() {
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    pdl_trigger();   // after the TMEM allocation
-  };
 
   if (warp < 2) {
-    join();
     // ---------------- MMA issuer of tile `warp`: the warp waits as one, an elected lane issues
     const int t = __shfl_sync(0xffffffffu, warp, 0);
     const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
@@ -620,7 +628,6 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     int kst = 0, vst = 0;            // stages, and the parities of their being empty
     uint32_t kph = 1, vph = 1;
     bool more = open();
-    join();
     while (more) {
       // K runs a block ahead of V, as S runs ahead of P V: the turns are K(0), K(1), V(0), K(2), V(1), ...
       check(id_v);
@@ -694,7 +701,6 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     }
     if (!ok) flags[0] = 1;
   } else {
-    join();
     const int t = (warp - 2) >> 2;
     uint32_t done = 0;
     while (walk.next(p, w)) {
@@ -795,10 +801,10 @@ attn_kv4_parts_kernel(const __grid_constant__ AttnKv4Params p, int blocks) {
     const int h = what.y * p.group + R % p.group;
     const float inv = all == 0.f ? 0.f : 1.f / all;
     uint4 out;
-    out.x = (uint32_t)f32_to_bf16_any(a.x * inv) | ((uint32_t)f32_to_bf16_any(a.y * inv) << 16);
-    out.y = (uint32_t)f32_to_bf16_any(a.z * inv) | ((uint32_t)f32_to_bf16_any(a.w * inv) << 16);
-    out.z = (uint32_t)f32_to_bf16_any(b.x * inv) | ((uint32_t)f32_to_bf16_any(b.y * inv) << 16);
-    out.w = (uint32_t)f32_to_bf16_any(b.z * inv) | ((uint32_t)f32_to_bf16_any(b.w * inv) << 16);
+    out.x = kv4_bf16_pair(a.x * inv, a.y * inv);
+    out.y = kv4_bf16_pair(a.z * inv, a.w * inv);
+    out.z = kv4_bf16_pair(b.x * inv, b.y * inv);
+    out.w = kv4_bf16_pair(b.z * inv, b.w * inv);
     *reinterpret_cast<uint4*>(p.out + t * p.o_tok + h * p.o_head + 8 * piece) = out;
     if (piece == 0 && p.lse != nullptr)
       p.lse[t * p.H + h] = all == 0.f ? -INFINITY : (mx + log2f(all)) * 0.6931471805599453f;

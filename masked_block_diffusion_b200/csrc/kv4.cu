@@ -112,15 +112,22 @@ struct AttnPlan {
   int tiles, n_splits, chunk;
   int nr;    // 8-row columns of the few-row kernel; 0: the tensor-core kernel
   bool cut;  // which may cut tiles into parts
+  int unit_shift;
 };
 
 // Up to 16 rows per KV head and request: the few-row kernel, 8 or 16 rows and a split of the keys per
 // block. More: the tensor-core kernel, which deals its work out by itself.
-AttnPlan attn_plan(int B, int max_q, int max_kv, int group, int Hkv) {
-  AttnPlan a{0, 1, 0, 0, max_kv > 512};
+AttnPlan attn_plan(int B, int T, int max_q, int max_kv, int group, int Hkv) {
+  AttnPlan a{0, 1, 0, 0, max_kv > 512, 0};
   const long rows = (long)max_q * group;
   a.nr = rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
-  if (a.nr == 0) return a;
+  if (a.nr == 0) {
+    // what the requests' work adds up to stays below 2^31
+    const long tiles = Hkv * std::min((long)B * ceil_div(rows, 256), (long)T * group / 256 + B);
+    while (tiles * (8 + (ceil_div(max_kv, 48) >> a.unit_shift)) >= 0x7FFFFFFFL && a.unit_shift < 30) ++a.unit_shift;
+    a.tiles = (int)std::min(tiles, 0x7FFFFFFFL);
+    return a;
+  }
   a.tiles = ceil_div(rows, 8 * a.nr);
   // Blocks that the GPU holds at a time, and blocks without a split.
   const long slots = kSMs * (a.nr == 1 ? 4 : 2);
@@ -309,7 +316,7 @@ int dllm_op_read_kv4(const dllm_kv4* cache, const int32_t* req, const int32_t* p
 long long dllm_op_attn_kv4_workspace(const dllm_kv4* cache, int B, int T, int max_q, int max_kv, int H) {
   if (!cache_ok(cache) || !attn_sizes_ok(cache, B, T, max_q, max_kv, H)) return DLLM_E_INVAL;
   if (B == 0 || max_q == 0) return 0;
-  const AttnPlan a = attn_plan(B, max_q, max_kv, H / cache->n_kv_heads, cache->n_kv_heads);
+  const AttnPlan a = attn_plan(B, T, max_q, max_kv, H / cache->n_kv_heads, cache->n_kv_heads);
   return (long long)attn_workspace(a, T, H, cache->head_dim);
 }
 
@@ -326,8 +333,9 @@ int dllm_op_attn_kv4(const dllm_kv4* cache, const uint16_t* q, long long q_token
       !vectors(out, DLLM_BF16, out_token_stride, out_head_stride) || !aligned16(workspace))
     return DLLM_E_INVAL;
   const int group = H / cache->n_kv_heads;
-  const AttnPlan a = attn_plan(B, max_q, max_kv, group, cache->n_kv_heads);
-  if ((long)cache->n_kv_heads * a.tiles > 65535) return DLLM_E_INVAL;   // the few-row kernel's grid
+  const AttnPlan a = attn_plan(B, T, max_q, max_kv, group, cache->n_kv_heads);
+  // the few-row kernel's grid; the tensor-core kernel's sums
+  if (a.nr ? (long)cache->n_kv_heads * a.tiles > 65535 : a.tiles > (1 << 27)) return DLLM_E_INVAL;
   if (attn_workspace(a, T, H, cache->head_dim) > (workspace ? workspace_bytes : 0)) return DLLM_E_INVAL;
   AttnKv4Params p;
   p.c = cache_of(cache);
@@ -359,6 +367,7 @@ int dllm_op_attn_kv4(const dllm_kv4* cache, const uint16_t* q, long long q_token
   const size_t part_rows = a.nr == 0 ? (size_t)kSMs * 512 : (size_t)a.n_splits * T * H;
   p.part_lse = p.part_o + part_rows * cache->head_dim;
   p.cut = a.cut;
+  p.unit_shift = a.unit_shift;
   p.parts = reinterpret_cast<int4*>(p.part_lse + part_rows);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = cache->head_dim == 176   ? run_attn<176>(st, a, p)
