@@ -55,6 +55,10 @@ DLLM_DEV bool elect_one() {
   return r != 0;
 }
 
+// What parts cost on their way to memory and back, in blocks of keys: 2 us and 180 KB each way per
+// part of head_dim 176, 4 TB/s.
+__host__ __device__ constexpr int kv4_cut_cost(int parts, int hd) { return 2 + parts * hd / 2600; }
+
 template <int HD>
 struct AttnKv4TcCfg {
   static constexpr int BK = HD == 64 ? 96 : 48;          // keys of a block
@@ -128,17 +132,22 @@ struct Kv4Work {
   Kv4Req rq;
 };
 
-// The work of a thread block, the same in all its threads: a share of all tiles' key blocks, which lie
-// request by request, head by head, from the last tile (which sees the most keys when causal) to the
-// first. Lengths are known on the device only, so each block adds up the requests' work by itself
-// (begin). If the caller's bounds say that tiles are short (cut = 0), the shares are of whole tiles. Else they are equal: 16 requests of 256 queries over 2176 to 4352 keys, 256 tiles on
-// 148 SMs, @@. With fewer tiles than blocks, each tile has as many shares as fit: one canvas, 16
-// tiles, in 9 shares each (shares that cut across tiles as well: @@).
+// The work of a thread block, the same in all its threads: a share of all tiles, which lie request by
+// request, head by head, from the last tile (which sees the most keys when causal) to the first.
+// Lengths are known on the device only, so each block adds up the requests' work by itself (begin).
+// The shares have either equal numbers of whole tiles or equal numbers of key blocks, and then some
+// tiles are cut into parts that attn_kv4_parts_kernel joins. A cut is worth its two parts' way to
+// memory and back if whole tiles would leave more SMs idle than that, which `begin` estimates (in key
+// blocks of 1.1 us at head_dim 176, 1.5 at 64). Measured, head_dim 176, whole against cut: one canvas of
+// 256 queries (16 tiles) over 256 keys 16.5 us and 18.1, 768 keys 26.4 and 19.7; 37 requests of 128 queries over
+// 500 to 1000 keys (296 tiles) 63 and 76; 16 canvases over 2200 to 4350 keys (256 tiles) 184 and 163.
+// With fewer tiles than SMs, every tile has as many shares as fit.
 template <int HD>
 struct Kv4Walk {
   using G = AttnKv4TcCfg<HD>;
   int b, h, i, x;           // the next tile, and how far into it the share begins
   int left, tiles;
+  bool cut;                 // shares may begin and end inside a tile
   Kv4Req rq;
 
   DLLM_DEV int blocks(const AttnKv4Params& p, int tile) const {
@@ -153,47 +162,64 @@ struct Kv4Walk {
   }
   // in units of 2^unit_shift key blocks, so that all of a call's fit 32 bits
   DLLM_DEV int cost(const AttnKv4Params& p, int tile) const {
-    return p.cut ? G::START + ((blocks(p, tile) + (1 << p.unit_shift) - 1) >> p.unit_shift) : 1;
+    return cut ? G::START + ((blocks(p, tile) + (1 << p.unit_shift) - 1) >> p.unit_shift) : 1;
   }
-  DLLM_DEV int costs(const AttnKv4Params& p) const {
-    if (!p.cut) return tiles;
+  DLLM_DEV int costs(const AttnKv4Params& p, int& most) const {
+    if (!cut) return tiles;
     int c = 0;
-    for (int t = 0; t < tiles; ++t) c += cost(p, t);
+    for (int t = 0; t < tiles; ++t) {
+      const int c1 = cost(p, t);
+      c += c1;
+      most = max(most, c1);
+    }
     return c;
   }
   // All threads; mem: MEM ints that stay as they are until the next barrier. Half of the time of a kernel that
   // has little to do is code that is fetched to run once, so 32 bits, few divisions and one barrier, which
   // serves as the kernel's too.
-  static constexpr int WARPS = G::THREADS / 32, MEM = 2 * WARPS + 8;
+  static constexpr int WARPS = G::THREADS / 32, MEM = 3 * WARPS + 8;
   DLLM_DEV void begin(const AttnKv4Params& p, int* mem) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r0 = p.B * tid / G::THREADS, r1 = p.B * (tid + 1) / G::THREADS;
-    int mine = 0, some = 0;
+    int work = 0, some = 0, most = 0;
+    cut = p.cut;
     for (int r = r0; r < r1; ++r) {
       request(p, r);
-      mine += p.c.Hkv * costs(p);
+      work += p.c.Hkv * costs(p, most);
       some += p.c.Hkv * tiles;
     }
-    some = __reduce_add_sync(0xffffffffu, some);
-    int upto = mine;
+    int upto_work = work, upto_some = some;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
+      const int v = __shfl_up_sync(0xffffffffu, upto_work, o), u = __shfl_up_sync(0xffffffffu, upto_some, o);
+      if (lane >= o) {
+        upto_work += v;
+        upto_some += u;
+      }
     }
+    most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 31) {
-      mem[warp] = upto;
-      mem[WARPS + warp] = some;
+      mem[warp] = upto_work;
+      mem[WARPS + warp] = upto_some;
+      mem[2 * WARPS + warp] = most;
     }
-    int* found = mem + 2 * WARPS;
+    int* found = mem + 3 * WARPS;
     __syncthreads();
-    // lane w of every warp adds up the warps before warp w
-    const int sum = lane < WARPS ? mem[lane] : 0;
-    const int count = __reduce_add_sync(0xffffffffu, lane < WARPS ? mem[WARPS + lane] : 0);
-    const int all = __reduce_add_sync(0xffffffffu, sum);
-    upto += __reduce_add_sync(0xffffffffu, lane < warp ? sum : 0);
+    // lane w of every warp has what warp w added up
+    const int sum = lane < WARPS ? mem[lane] : 0, tile_sum = lane < WARPS ? mem[WARPS + lane] : 0;
+    const int count = __reduce_add_sync(0xffffffffu, tile_sum);
+    int all = __reduce_add_sync(0xffffffffu, sum), n = gridDim.x;
+    if (cut) {
+      most = __reduce_max_sync(0xffffffffu, lane < WARPS ? mem[2 * WARPS + lane] : 0);
+      // tiles that are cut have to be worth it: parts are written and read again
+      cut = (count + n - 1) / n * most > all / n + (kv4_cut_cost(count < n ? n : 2 * n, HD) >> p.unit_shift);
+    }
+    if (!cut) all = count;
+    const int mine = cut ? work : some;
+    const int upto = (cut ? upto_work : upto_some) + __reduce_add_sync(0xffffffffu, lane < warp ? (cut ? sum : tile_sum) : 0);
     // no share is empty but the last blocks', so that a tile's parts lie in consecutive blocks
-    int n = min(all, (int)gridDim.x), lo = 0;
+    int lo = 0;
+    n = min(all, n);
     left = 0;
     if (count > 0 && count < n) n = n / count * count;
     if ((int)blockIdx.x < n) {
@@ -205,7 +231,7 @@ struct Kv4Walk {
       int rest = lo - (upto - mine);
       for (int r = r0; r < r1; ++r) {
         request(p, r);
-        const int c = costs(p);
+        const int c = costs(p, most);
         if (rest >= p.c.Hkv * c) {
           rest -= p.c.Hkv * c;
           continue;
@@ -246,8 +272,8 @@ struct Kv4Walk {
         continue;
       }
       const int all = blocks(p, i), take = min(left, cost(p, i) - x);
-      const int j0 = p.cut ? max(0, x - G::START) << p.unit_shift : 0;
-      const int j1 = p.cut ? min(all, max(0, x + take - G::START) << p.unit_shift) : all;
+      const int j0 = cut ? max(0, x - G::START) << p.unit_shift : 0;
+      const int j1 = cut ? min(all, max(0, x + take - G::START) << p.unit_shift) : all;
       const bool begun = x == 0;
       w = Kv4Work{b, h, i, j0, j1, j0 == 0, j1 == all, rq};
       left -= take;
