@@ -2,9 +2,11 @@
 // prompt pieces: many query rows per KV head. The rows, masks and results are those of
 // attention_kv4.cuh.
 //
-// One block takes 256 query rows (two tiles of 128) of one KV head over one split of the
-// keys. Both tiles read the same unpacked K and V, which halves the unpacking, and while one
-// tile's softmax turns its scores into weights the tensor pipe runs the other's products.
+// The work is cut into tiles of 256 query rows of one KV head, two halves of 128 (below: tile 0 and tile 1
+// of the tensor cores). Both read the same unpacked K and V, which halves the unpacking, and while
+// one's softmax turns its scores into weights the tensor pipe runs the other's products. One block
+// per SM goes through its share of all tiles (Kv4Walk); its unpacking warps begin the next tile while
+// the softmax still writes the last one out.
 //
 // Roles (512 threads):
 //   warps 0, 1   each issues one tile's products (warp 0 holds the TMEM allocation): S_t = Q_t K^T
@@ -15,8 +17,9 @@
 //                scores are ready when its softmax is.
 //   warps 2..5   softmax of tile 0, warps 6..9 of tile 1: one row per thread (TMEM lane), 48
 //                scores in registers, lazy reference as in attention_kv4.cuh; O is rescaled in
-//                TMEM when the reference moves (rare). They load their rows of Q first, and
-//                write O out through the same shared memory in the end, both along the rows.
+//                TMEM when the reference moves (rare). They copy their rows of Q first, and
+//                write O out through the same shared memory in the end, both along the rows;
+//                a part of a tile leaves in fp32 straight from TMEM, [hd / 4][row][4].
 //   warps 10..15 unpack 8 (of 96 keys: 16) keys of each block, K to bf16 and V to sixteenths in
 //                fp16 (both exact), as 64-dim atoms of 128-byte rows with the 128-byte swizzle
 //                (K's rows are keys, K-major; V's are the same rows read as the MN-major operand).
@@ -27,8 +30,13 @@
 // fits, in multiples of 48, so that six warps unpack: 96 at head_dim 64, else 48.
 // The code has to stay within the instruction cache: three roles run different loops at a time, and
 // with the unrolled forms of loading Q and writing O (150 KB of code in all) every loop ran a
-// quarter slower. What runs once per block is therefore not unrolled.
-// Every wait is bounded, as in gemm_tc.cuh; a block that gives one up writes NaN.
+// quarter slower, and code that runs once waits for its own fetching. What runs once per tile is
+// therefore small loops. At head_dim 176 a block of 48 keys takes 1.1 us, of which the products alone need
+// 0.8 (Q is read from shared memory again for every 48 keys); at head_dim 64 a block of 96 keys takes 1.5,
+// and 256 x 96 exponentials alone 0.8.
+// 37 requests of 128 queries over 2048 keys at head_dim 176: 110 us, 990 TFLOP/s. 16 canvases of 256
+// queries over 2200 to 4350 keys: 164 us, 915 TFLOP/s; at head_dim 64, 148 us, 494 TFLOP/s.
+// Every wait is bounded, as in gemm_tc.cuh; a block that gives one up writes NaN from there on.
 #pragma once
 
 #include "attention_kv4.cuh"
@@ -140,7 +148,7 @@ struct Kv4Work {
 // memory and back if whole tiles would leave more SMs idle than that, which `begin` estimates (in key
 // blocks of 1.1 us at head_dim 176, 1.5 at 64). Measured, head_dim 176, whole against cut: one canvas of
 // 256 queries (16 tiles) over 256 keys 16.5 us and 18.1, 768 keys 26.4 and 19.7; 37 requests of 128 queries over
-// 500 to 1000 keys (296 tiles) 63 and 76; 16 canvases over 2200 to 4350 keys (256 tiles) 184 and 163.
+// 500 to 1000 keys (296 tiles) 63 and 76; 16 canvases over 2200 to 4350 keys (256 tiles) 209 and 164.
 // With fewer tiles than SMs, every tile has as many shares as fit.
 template <int HD>
 struct Kv4Walk {
