@@ -206,12 +206,13 @@ struct Kv4Walk {
       }
     }
     most = __reduce_max_sync(0xffffffffu, most);
+    int* found = mem + 3 * WARPS;
+    if (tid == 0) found[0] = -1;
     if (lane == 31) {
       mem[warp] = upto_work;
       mem[WARPS + warp] = upto_some;
       mem[2 * WARPS + warp] = most;
     }
-    int* found = mem + 3 * WARPS;
     __syncthreads();
     // lane w of every warp has what warp w added up
     const int sum = lane < WARPS ? mem[lane] : 0, tile_sum = lane < WARPS ? mem[WARPS + lane] : 0;
@@ -262,6 +263,7 @@ struct Kv4Walk {
     __syncthreads();
     tc_fence_after();
     b = found[0];
+    if (b < 0) left = 0;   // no work (or row ranges that overlap, in numbers beyond 32 bits)
     h = found[1];
     i = found[2];
     x = found[3];
@@ -271,10 +273,16 @@ struct Kv4Walk {
   DLLM_DEV bool next(const AttnKv4Params& p, Kv4Work& w) {
     while (left > 0) {
       if (i < 0) {
-        if (++h == p.c.Hkv) {
+        if (++h == p.c.Hkv) {   // the next request with rows: a padded batch may have many without
           h = 0;
-          if (++b >= p.B) return false;
-          request(p, b);
+          const int lane = threadIdx.x & 31;
+          unsigned some = 0;
+          for (++b; some == 0; b += 32) {
+            if (b >= p.B) return false;
+            const int r = min(b + lane, p.B - 1);
+            some = __ballot_sync(0xffffffffu, b + lane < p.B && p.q_start[r + 1] > p.q_start[r]);
+          }
+          request(p, b - 32 + __ffs(some) - 1);
         }
         i = tiles - 1;
         continue;

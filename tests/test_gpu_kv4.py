@@ -415,6 +415,15 @@ def test_attention_of_one_tile_among_many_empty_requests(d, keys, n):
     attend_case(d, 2, 1, 64, queries, lens, True, seed=26)
 
 
+def test_attention_of_requests_far_apart_in_a_padded_batch():
+    B = 300
+    queries, lens = [0] * B, [3] * B
+    for i, n, m in ((0, 40, 900), (31, 1, 1), (32, 70, 2500), (170, 33, 700), (299, 150, 1200)):
+        queries[i], lens[i] = n, m
+    attend_case(176, 4, 2, 32, queries, lens, True, seed=28)
+    attend_case(64, 4, 2, 32, queries, lens, False, seed=29)
+
+
 def test_attention_of_many_tiles_answers_bad_requests_with_nan():
     rng = np.random.default_rng(27)
     B, queries, keys, page, h, hk, d = 40, 70, 300, 32, 4, 2, 64
