@@ -217,19 +217,22 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
   __syncthreads();
 
   // Copies stage `it` (first warp): lane i takes piece i, a page's share of it. False if its stage did
-  // not come free.
-  auto copy_stage = [&](int it) -> bool {
-    const int shift = min(p.c.page_shift, 7);
-    const int keys = 1 << shift;
+  // not come free. The page ids of a stage are asked for when the one before is copied.
+  const int shift = min(p.c.page_shift, 7), keys = 1 << shift;
+  auto piece = [&](int t) -> bool { return lane < (G::KEYS >> shift) && t < ke; };
+  auto ask = [&](int it) -> int {
     const int t = ks + it * G::KEYS + lane * keys;
-    int id = -1;
-    if (lane < (G::KEYS >> shift) && t < ke) {
-      id = p.table[(long)b * p.stride + (t >> p.c.page_shift)];
-      if (id < 0 || id >= p.c.n_pages) {
-        id = -1;
-        flags[1] = 1;
-      }
+    return piece(t) ? p.table[(long)b * p.stride + (t >> p.c.page_shift)] : 0;
+  };
+  int id_next = warp == 0 ? ask(0) : 0;
+  auto copy_stage = [&](int it) -> bool {
+    const int t = ks + it * G::KEYS + lane * keys;
+    int id = piece(t) ? id_next : -1;
+    if (piece(t) && (id < 0 || id >= p.c.n_pages)) {
+      id = -1;
+      flags[1] = 1;
     }
+    id_next = ask(it + 1);
     const uint32_t codes = keys * (HD / 2), scales = keys * (HD / 16);
     const uint32_t n = __popc(__ballot_sync(0xffffffffu, id >= 0));
     const int st = it % G::STAGES;
