@@ -13,8 +13,10 @@
 //                (bf16) into tile t's S columns, and O_t += P_t V (fp16) with P_t read from
 //                TMEM. A wait and an issue cost such a warp 150 to 200 cycles each among the
 //                busy warps of its scheduler, so one warp for both tiles was the bottleneck.
-//                S_t(j + 1) goes out as soon as the softmax has read S_t(j), so a tile's next
-//                scores are ready when its softmax is.
+//                With two buffers of scores per tile (head_dim 64 and 128) S_t(j + 2) goes out when
+//                O_t(j) is done, whose P_t(j) lay in the same columns; with one, S_t(j + 1) goes out as
+//                soon as the softmax has read S_t(j). Either way a tile's next scores are there
+//                when its softmax is.
 //   warps 2..5   softmax of tile 0, warps 6..9 of tile 1: one row per thread (TMEM lane), 48
 //                scores in registers, lazy reference as in attention_kv4.cuh; O is rescaled in
 //                TMEM when the reference moves (rare). They copy their rows of Q first, and
@@ -26,16 +28,17 @@
 //                Eight consecutive lanes write 4 groups of 2 adjacent keys: 8 different 16-byte
 //                columns, no bank conflict. The packed bytes come straight into registers, a block
 //                of keys ahead, and the page ids two blocks ahead.
-// TMEM: S_0, S_1 (BK columns each), P_0, P_1 (BK / 2), O_0, O_1 (head_dim). Keys per block: what
-// fits, in multiples of 48, so that six warps unpack: 96 at head_dim 64, else 48.
+// TMEM: S_0, S_1 (BK columns each, or two times BK), P_0, P_1 (BK / 2, or in S), O_0, O_1 (head_dim). Keys per
+// block: what fits, in multiples of 48, so that six warps unpack: 96 at head_dim 64, else 48.
 // The code has to stay within the instruction cache: three roles run different loops at a time, and
 // with the unrolled forms of loading Q and writing O (150 KB of code in all) every loop ran a
 // quarter slower, and code that runs once waits for its own fetching. What runs once per tile is
 // therefore small loops. At head_dim 176 a block of 48 keys takes 1.1 us, of which the products alone need
-// 0.8 (Q is read from shared memory again for every 48 keys); at head_dim 64 a block of 96 keys takes 1.5,
+// 0.8 (Q is read from shared memory again for every 48 keys); at head_dim 64 a block of 96 keys takes 1.4,
 // and 256 x 96 exponentials alone 0.8.
 // 37 requests of 128 queries over 2048 keys at head_dim 176: 110 us, 990 TFLOP/s. 16 canvases of 256
-// queries over 2200 to 4350 keys: 164 us, 915 TFLOP/s; at head_dim 64, 148 us, 494 TFLOP/s.
+// queries over 2200 to 4350 keys: 164 us, 915 TFLOP/s; at head_dim 64, 139 us, 525 TFLOP/s
+// (148 with one buffer of scores per tile; head_dim 128: 176 and 188).
 // Every wait is bounded, as in gemm_tc.cuh; a block that gives one up writes NaN from there on.
 #pragma once
 
@@ -81,8 +84,18 @@ struct AttnKv4TcCfg {
   static constexpr int kOffBar = kOffV + VST * kKV;
   static constexpr int kOffShare = kOffBar + 256;        // Kv4Walk::begin's
   static constexpr int kTotal = kOffShare + 256 + 1024;
-  static constexpr int kPCol = 2 * BK;
-  static constexpr int kOCol = 3 * BK;
+  // Two buffers of scores per tile, P in place of the scores it came from, where TMEM has room; else one, and P
+  // in columns of its own.
+  static constexpr bool TWO = 4 * BK + 2 * HD <= 512;
+  static constexpr int kOCol = (TWO ? 4 : 3) * BK;
+  __host__ __device__ static constexpr int s_col(int t, uint32_t c) { return TWO ? (2 * t + (int)(c & 1)) * BK : t * BK; }
+  // the column of a tile's P from key `key` of a block on (a multiple of 16)
+  __host__ __device__ static constexpr int p_col(int t, uint32_t c, int key) {
+    return TWO ? s_col(t, c) + key / CH * CH + key % CH / 2 : 2 * BK + t * (BK / 2) + key / 2;
+  }
+  // which of a tile's two barriers counts block c, and its phase's parity
+  __host__ __device__ static constexpr int bar(int t, uint32_t c) { return 2 * t + (TWO ? (int)(c & 1) : 0); }
+  __host__ __device__ static constexpr uint32_t par(uint32_t c) { return TWO ? (c >> 1) & 1 : c & 1; }
   static constexpr int kTmemCols = 512;
   static constexpr int UNPACK = 6;                       // unpacking warps
   static constexpr int GPW = BK / 8 / UNPACK;            // groups of 8 keys of a block that each takes
@@ -332,15 +345,14 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const u
   }
   const float fac = p.scale_log2;
   const uint32_t lane_base = *tmem_slot + ((uint32_t)row0 << 16);
-  const uint32_t s_col = lane_base + t * BK;
-  const uint32_t p_col = lane_base + G::kPCol + t * (BK / 2);
   const uint32_t o_col = lane_base + G::kOCol + t * HD;
   float m = -INFINITY, l = 0.f;
   bool ok = true;
 #pragma unroll 1
   for (int j = 0; j < nblk; ++j) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], (done + j) & 1, flags))) { ok = false; break; }
+    if (!__all_sync(0xffffffffu, mbar_wait(&s_full[G::bar(t, done + j)], G::par(done + j), flags))) { ok = false; break; }
     tc_fence_after();
+    const uint32_t s_col = lane_base + G::s_col(t, done + j);
     float s[CH];
     const int seen = lim - (ks + j * BK);
     auto load = [&](int q) {
@@ -365,7 +377,7 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const u
       const bool need = mx > m + (kKv4Low + 8.f);
       if (__any_sync(0xffffffffu, need)) {
         // O is stable once the product of the block before is done
-        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[t], (done + j - 1) & 1, flags))) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[G::bar(t, done + j - 1)], G::par(done + j - 1), flags))) { ok = false; break; }
         tc_fence_after();
         const float mn = need ? mx - kKv4Low : m;
         const float f = need ? exp2f(m - mn) : 1.0f;
@@ -387,7 +399,7 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const u
 #pragma unroll
     for (int q = NCH - 1; q >= 0; --q) {   // the last chunk is still in registers
       if (q < NCH - 1) load(q);
-      if (q == 0) {
+      if (q == 0 && !G::TWO) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_read[t]);
@@ -403,11 +415,11 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const u
         const __half2 h = __floats2half2_rn(a, b);
         pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
       }
-      if (q == NCH - 1 && j > 0) {   // P's columns are free once the product of the block before is done
-        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[t], (done + j - 1) & 1, flags))) { ok = false; break; }
+      if (q == NCH - 1 && j > 0 && !G::TWO) {   // P's columns are free once the product of the block before is done
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[G::bar(t, done + j - 1)], G::par(done + j - 1), flags))) { ok = false; break; }
         tc_fence_after();
       }
-      kv4_store_weights(p_col + q * (CH / 2), pk);
+      kv4_store_weights(lane_base + G::p_col(t, done + j, q * CH), pk);
     }
     if (!ok) break;
     float l0, l1;
@@ -416,9 +428,9 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const u
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&p_full[t]);
+    if (lane == 0) mbar_arrive(&p_full[G::bar(t, done + j)]);
   }
-  if (ok && nblk > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], (done + nblk - 1) & 1, flags));
+  if (ok && nblk > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[G::bar(t, done + nblk - 1)], G::par(done + nblk - 1), flags));
   if (!ok) flags[0] = 1;
   tc_fence_after();
   const bool lost = flags[0] != 0;
@@ -489,11 +501,12 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
   uint64_t* k_empty = k_full + KST;
   uint64_t* v_full = k_empty + KST;
   uint64_t* v_empty = v_full + VST;
-  uint64_t* s_full = v_empty + VST;  // [2]: S_t(j) is in its columns
-  uint64_t* s_read = s_full + 2;     // [2]: the softmax has it in registers
-  uint64_t* p_full = s_read + 2;     // [2]: P_t(j) is in its columns
-  uint64_t* pv_done = p_full + 2;    // [2]: P_t V(j) completed
-  uint64_t* q_full = pv_done + 2;    // [2]: tile t's Q is in shared memory
+  // two per tile, of even and odd blocks, with two buffers (G::bar)
+  uint64_t* s_full = v_empty + VST;  // [4]: S_t(j) is in its columns
+  uint64_t* p_full = s_full + 4;     // [4]: P_t(j) is in its columns
+  uint64_t* pv_done = p_full + 4;    // [4]: P_t V(j) completed
+  uint64_t* s_read = pv_done + 4;    // [2]: the softmax has S_t(j) in registers (one buffer only)
+  uint64_t* q_full = s_read + 2;     // [2]: tile t's Q is in shared memory
   uint64_t* drain = q_full + 2;      // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [0] abort
@@ -509,10 +522,12 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
       mbar_init(&v_empty[s], 2);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&s_full[t], 1);
+      for (int k = 2 * t; k < 2 * t + 2; ++k) {
+        mbar_init(&s_full[k], 1);
+        mbar_init(&p_full[k], 4);
+        mbar_init(&pv_done[k], 1);
+      }
       mbar_init(&s_read[t], 4);
-      mbar_init(&p_full[t], 4);
-      mbar_init(&pv_done[t], 1);
       mbar_init(&q_full[t], 4);
       mbar_init(&drain[t], 1);
     }
@@ -536,7 +551,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     // ---------------- MMA issuer of tile `warp`: the warp waits as one, an elected lane issues
     const int t = __shfl_sync(0xffffffffu, warp, 0);
     const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    const uint32_t s_col = tm + t * BK, p_col = tm + G::kPCol + t * (BK / 2), o_col = tm + G::kOCol + t * HD;
+    const uint32_t o_col = tm + G::kOCol + t * HD;
     const uint64_t qd = sdesc_k_sw128(smem_u32(smem + t * G::kQTile));
     const uint64_t kd0 = sdesc_k_sw128(smem_u32(sK)), vd0 = sdesc_mn_sw128(smem_u32(sV), G::kAtom);
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -546,7 +561,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     uint32_t kph = 0, vph = 0;
     uint32_t done = 0, loads = 0;
     bool live = true;            // the work has rows in this tile; otherwise the stages are only passed on
-    auto issue_s = [&]() -> bool {
+    auto issue_s = [&](int j) -> bool {
       if (!wait(&k_full[kst], kph)) return false;
       tc_fence_after();
       if (elect_one()) {
@@ -554,9 +569,9 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
           const uint64_t kd = kd0 + kst * (G::kKV >> 4);   // descriptors count 16-byte units
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k)
-            umma_bf16(s_col, qd + (((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4),
+            umma_bf16(tm + G::s_col(t, done + j), qd + (((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4),
                       kd + (((k >> 2) * G::kAtom + (k & 3) * 32) >> 4), kIdQK, k != 0);
-          umma_commit(&s_full[t]);
+          umma_commit(&s_full[G::bar(t, done + j)]);
           umma_commit(&k_empty[kst]);
         } else {
           mbar_arrive(&k_empty[kst]);
@@ -574,19 +589,19 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
         if (live && !w.rq.bad) ++loads;
         continue;
       }
-      ok = (!live || wait(&q_full[t], loads & 1)) && issue_s();
+      ok = (!live || wait(&q_full[t], loads & 1)) && issue_s(0) && (!G::TWO || nblk == 1 || issue_s(1));
 #pragma unroll 1
       for (int j = 0; j < nblk && ok; ++j) {
-        if (j + 1 < nblk && !((!live || wait(&s_read[t], (done + j) & 1)) && issue_s())) { ok = false; break; }
-        if (!wait(&v_full[vst], vph) || (live && !wait(&p_full[t], (done + j) & 1))) { ok = false; break; }
+        if (!G::TWO && j + 1 < nblk && !((!live || wait(&s_read[t], (done + j) & 1)) && issue_s(j + 1))) { ok = false; break; }
+        if (!wait(&v_full[vst], vph) || (live && !wait(&p_full[G::bar(t, done + j)], G::par(done + j)))) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
           if (live) {
             const uint64_t vd = vd0 + vst * (G::kKV >> 4);
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k)
-              umma_bf16_ts(o_col, p_col + k * 8, vd + ((k * 16 * 128) >> 4), kIdPV, (j | k) != 0);
-            umma_commit(&pv_done[t]);
+              umma_bf16_ts(o_col, tm + G::p_col(t, done + j, 16 * k), vd + ((k * 16 * 128) >> 4), kIdPV, (j | k) != 0);
+            umma_commit(&pv_done[G::bar(t, done + j)]);
             umma_commit(&v_empty[vst]);
           } else {
             mbar_arrive(&v_empty[vst]);
@@ -594,6 +609,9 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
         }
         __syncwarp();
         if (++vst == VST) { vst = 0; vph ^= 1; }
+        // the next scores of this buffer once P_t(j), which lies in it, has been read
+        if (G::TWO && j + 2 < nblk)
+          ok = (!live || wait(&pv_done[G::bar(t, done + j)], G::par(done + j))) && issue_s(j + 2);
       }
       if (live) {
         done += nblk;
