@@ -159,7 +159,7 @@ struct Kv4Work {
 // The shares have either equal numbers of whole tiles or equal numbers of key blocks, and then some
 // tiles are cut into parts that attn_kv4_parts_kernel joins. A cut is worth its two parts' way to
 // memory and back if whole tiles would leave more SMs idle than that, which `begin` estimates (in key
-// blocks of 1.1 us at head_dim 176, 1.5 at 64). Measured, head_dim 176, whole against cut: one canvas of
+// blocks of 1.1 us at head_dim 176, 1.4 at 64). Measured, head_dim 176, whole against cut: one canvas of
 // 256 queries (16 tiles) over 256 keys 16.5 us and 18.1, 768 keys 26.4 and 19.7; 37 requests of 128 queries over
 // 500 to 1000 keys (296 tiles) 63 and 76; 16 canvases over 2200 to 4350 keys (256 tiles) 209 and 164.
 // With fewer tiles than SMs, every tile has as many shares as fit.
