@@ -132,7 +132,8 @@ DLLM_DEV uint32_t kv4_pack8(float (&v)[8], int& byte) {
 // neighbouring lanes a group, so that loads of 32 or 16 bytes and stores of 4 are contiguous along
 // a warp. The loads of all its tokens go out first, before the page ids (two dependent loads) and the
 // cos and sin are there; a rotated chunk's partner comes later, out of the L1 cache, where
-// another thread's load has brought it.
+// another thread's load has brought it. Bound by instruction issue (68% while SMs are busy): 10 600
+// tokens of 8 heads of 176 in bf16, three prompts, 38 us (26 without rotation), 77 MB; 64 tokens 3.3 us.
 template <int HD, typename TI, bool VEC>
 __global__ void __launch_bounds__(512, sizeof(TI) == 2 ? 3 : 2)
 kv4_append_kernel(const __grid_constant__ RopeParams r, Kv4 c, Kv4Addr a, const TI* __restrict__ k, long k_tok,
@@ -247,7 +248,8 @@ DLLM_DEV __nv_bfloat162 kv4_scale_bf16x2(uint32_t byte) {
 
 // Reads T tokens' rows back as bf16 [T][Hkv][hd]. One warp per token, lanes along its groups of 16
 // dims (K's heads, then V's), whose loads are all issued before the first is used. A token with no
-// page reads NaN; a padding token's rows are zeroed or left as they are.
+// page reads NaN; a padding token's rows are zeroed or left as they are. Bound by its writes: 52 600
+// positions of 8 heads of 176 80 us, 4.7 TB/s (a torch fill of what it writes takes 77 us).
 template <int HD>
 __global__ void __launch_bounds__(256)
 kv4_read_kernel(Kv4 c, Kv4Addr a, int T, bf16_t* __restrict__ k_out, bf16_t* __restrict__ v_out, int zero_padding) {
