@@ -50,7 +50,7 @@ struct AttnKv4Params {
   const int* table;         // [B][stride]
   int stride, B, T, H, group;
   int max_q, max_kv, causal;
-  int n_splits, chunk;      // keys [i chunk, (i + 1) chunk) belong to split i
+  int n_splits;
   float scale_log2;         // scale * log2(e)
   float* part_o;            // [n_splits][T][H][hd]
   float* part_lse;          // [n_splits][T][H], log2 domain
@@ -205,8 +205,10 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
   }
   if (R0 >= n_rows) return;
   const int last = min(n_rows - 1, R0 + G::kRows - 1);
-  const int ks = sp * p.chunk;
-  const int ke = min(kv4_row_limit(p, rq, last / p.group), ks + p.chunk);
+  // equal splits of the request's own keys, in whole stages: max_kv may lie far above them
+  const int chunk = max(1, ((rq.kv + p.n_splits - 1) / p.n_splits + G::KEYS - 1) / G::KEYS) * G::KEYS;
+  const int ks = sp * chunk;
+  const int ke = min(kv4_row_limit(p, rq, last / p.group), ks + chunk);
   const int nst = ke > ks ? (ke - ks + G::KEYS - 1) / G::KEYS : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 

@@ -109,7 +109,7 @@ bool addr_ok(const int32_t* req, const int32_t* pos, const int32_t* table, int n
 // ---- attention: how a call is cut up
 
 struct AttnPlan {
-  int tiles, n_splits, chunk;
+  int tiles, n_splits;
   int nr;    // 8-row columns of the few-row kernel; 0: the tensor-core kernel
   bool cut;  // which may cut tiles into parts
   int unit_shift;
@@ -118,7 +118,7 @@ struct AttnPlan {
 // Up to 16 rows per KV head and request: the few-row kernel, 8 or 16 rows and a split of the keys per
 // block. More: the tensor-core kernel, which deals its work out by itself.
 AttnPlan attn_plan(int B, int T, int max_q, int max_kv, int group, int Hkv, int hd) {
-  AttnPlan a{0, 1, 0, 0, false, 0};
+  AttnPlan a{0, 1, 0, false, 0};
   const long rows = (long)max_q * group;
   a.nr = rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
   if (a.nr == 0) {
@@ -147,9 +147,8 @@ AttnPlan attn_plan(int B, int T, int max_q, int max_kv, int group, int Hkv, int 
     want = blocks >= slots / 4 ? std::min<long>(ceil_div(2 * slots, blocks), ceil_div(max_kv, 512)) : slots / blocks;
   }
   want = std::max(1L, std::min<long>(want, ceil_div(max_kv, 64)));
-  const int grain = 128;   // keys of a stage
-  a.chunk = std::max(grain, ceil_div(ceil_div(max_kv, want), grain) * grain);
-  a.n_splits = std::max(1, ceil_div(max_kv, a.chunk));
+  const int stage = 128;   // keys; no more splits than there are stages, or fill them
+  a.n_splits = std::max(1, ceil_div(max_kv, std::max(stage, ceil_div(ceil_div(max_kv, want), stage) * stage)));
   return a;
 }
 
@@ -364,7 +363,6 @@ int dllm_op_attn_kv4(const dllm_kv4* cache, const uint16_t* q, long long q_token
   p.max_kv = max_kv;
   p.causal = causal != 0;
   p.n_splits = a.n_splits;
-  p.chunk = a.chunk;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.mask_low = 0x003C003Cu;
   p.mask_high = 0x03C003C0u;

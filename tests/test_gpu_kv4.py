@@ -415,6 +415,20 @@ def test_attention_of_one_tile_among_many_empty_requests(d, keys, n):
     attend_case(d, 2, 1, 64, queries, lens, True, seed=26)
 
 
+@pytest.mark.parametrize("queries", [1, 8, 40])
+def test_attention_with_the_widest_bounds(queries):
+    """Bounds far above the lengths: the work is shared out in coarser units, and splits are mostly empty."""
+    rng = np.random.default_rng(30)
+    B, h, hk, d = 100, 8, 4, 64
+    keys = [int(n) for n in rng.integers(1, 300, B)]
+    keys[3], keys[70] = 2000, 1500
+    cache, table, held = filled(rng, keys, 32, hk, d)
+    q = torch.tensor(rng.normal(size=(B * queries, h, d)), device="cuda").bfloat16()
+    out, lse = cache.attend(q, i32(np.arange(B + 1) * queries), i32(keys), i32(table), max_q=queries, max_kv=(1 << 29) - 1,
+                            causal=False, return_lse=True)
+    check_attention(out, lse, q, held, [queries] * B, keys, False, d ** -0.5)
+
+
 def test_attention_of_requests_far_apart_in_a_padded_batch():
     B = 300
     queries, lens = [0] * B, [3] * B
