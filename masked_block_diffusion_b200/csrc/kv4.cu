@@ -142,9 +142,10 @@ AttnPlan attn_plan(int B, int T, int max_q, int max_kv, int group, int Hkv, int 
   if (blocks * ceil_div(max_kv, 256) <= slots) {
     want = ceil_div(max_kv, 256);                      // a short call: as wide as it goes
   } else {
-    // one wave of blocks when a few requests share the GPU; else blocks of 512 keys or more and
-    // about two waves of them, so that requests of different lengths even out
-    want = blocks >= slots / 4 ? std::min<long>(ceil_div(2 * slots, blocks), ceil_div(max_kv, 512)) : slots / blocks;
+    // One wave of blocks if every tile has two splits or more in it: 24 tokens over up to 4352 keys (192 tiles of 8 KV
+    // heads) 50 us in 3 splits, 57 in 7. Else about two waves, of 512 keys or more per block, so that requests of
+    // different lengths even out: 64 tokens (512 tiles) 111 us in 3 splits, 116 in 1.
+    want = 2 * blocks <= slots ? slots / blocks : std::min<long>(ceil_div(2 * slots, blocks), ceil_div(max_kv, 512));
   }
   want = std::max(1L, std::min<long>(want, ceil_div(max_kv, 64)));
   const int stage = 128;   // keys; no more splits than there are stages, or fill them
