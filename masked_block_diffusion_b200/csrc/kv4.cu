@@ -136,7 +136,9 @@ AttnPlan attn_plan(int B, int T, int max_q, int max_kv, int group, int Hkv, int 
   }
   a.tiles = ceil_div(rows, 8 * a.nr);
   // Blocks that the GPU holds at a time, and blocks without a split.
-  const long slots = kSMs * (a.nr == 1 ? 4 : 2);
+  const long slots = kSMs * (a.nr == 1   ? AttnKv4Cfg<64, 1>::BLOCKS
+                             : hd == 176 ? AttnKv4Cfg<176, 2>::BLOCKS
+                                         : AttnKv4Cfg<64, 2>::BLOCKS);
   const long blocks = (long)B * Hkv * a.tiles;
   long want;
   if (blocks * ceil_div(max_kv, 256) <= slots) {
