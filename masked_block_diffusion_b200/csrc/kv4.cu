@@ -115,12 +115,16 @@ struct AttnPlan {
   int unit_shift;
 };
 
-// Up to 16 rows per KV head and request: the few-row kernel, 8 or 16 rows and a split of the keys per
-// block. More: the tensor-core kernel, which deals its work out by itself.
+// Few rows per KV head and request: the few-row kernel, 8 or 16 rows and a split of the keys per block.
+// More: the tensor-core kernel, which deals its work out by itself.
 AttnPlan attn_plan(int B, int T, int max_q, int max_kv, int group, int Hkv, int hd) {
   AttnPlan a{0, 1, 0, false, 0};
   const long rows = (long)max_q * group;
-  a.nr = rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
+  // Two tiles of 16 rows unpack the cache twice, which at head_dim 64 and 128 is still faster than a tile of 256 rows
+  // that is mostly empty: 32 rows of 8 KV heads over up to 4352 keys, 1, 8 and 64 requests, at head_dim 64 13, 31 and
+  // 144 us against 19, 37 and 158, at 128 17, 42 and 204 against 21, 43 and 232, but at 176 22, 60 and 311 against 22,
+  // 52 and 278; and 48 rows at head_dim 64 16, 40 and 184 against 19, 32 and 161.
+  a.nr = rows <= 8 ? 1 : rows <= (hd == 176 ? 16 : 32) ? 2 : 0;
   if (a.nr == 0) {
     // what the requests' work adds up to stays below 2^31
     const long tiles = Hkv * std::min((long)B * ceil_div(rows, 256), (long)T * group / 256 + B);

@@ -387,6 +387,14 @@ def test_attention_split_canvas():
     attend_case(176, 4, 2, 64, [40, 17], [3001, 1290], False, seed=21)
 
 
+@pytest.mark.parametrize("d", [64, 128, 176])
+@pytest.mark.parametrize("queries", [8, 9])
+def test_attention_around_the_kernels_border(d, queries):
+    """32 and 36 rows per KV head, of which some requests fill one tile and a part of another, or none."""
+    attend_case(d, 8, 2, 32, [queries, 5, 3, 0, 1, queries], [700, 1500, 3, 9, 40, 2], True, seed=31)
+    attend_case(d, 8, 2, 32, [queries, 4, queries], [90, 2600, 0], False, seed=32)
+
+
 @pytest.mark.parametrize("d,keys", [(64, 10000), (128, 5000), (176, 7000)])
 def test_attention_of_one_tile_in_many_splits(d, keys):
     """One KV head and few rows: more splits than a warp has lanes."""
