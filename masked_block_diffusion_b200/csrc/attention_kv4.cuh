@@ -1,5 +1,5 @@
 // Attention over the paged 4-bit KV cache for few query rows per KV head (single tokens, a
-// few tokens to verify, small canvases), and the merge of key splits.
+// few tokens to verify, small canvases), and the merge of key splits. What both attention kernels share is here.
 //
 // Row R of request b and KV head g is query R / group, head g * group + R % group. Row R
 // sees the keys below lim = kv_len (causal: kv_len - n + R / group + 1 for n queries):
@@ -50,7 +50,7 @@ struct AttnKv4Params {
   const int* table;         // [B][stride]
   int stride, B, T, H, group;
   int max_q, max_kv, causal;
-  int n_splits;
+  int n_splits;             // few rows: blocks that a request's keys are shared out to, in equal parts
   float scale_log2;         // scale * log2(e)
   float* part_o;            // [n_splits][T][H][hd]
   float* part_lse;          // [n_splits][T][H], log2 domain
