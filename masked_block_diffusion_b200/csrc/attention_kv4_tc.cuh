@@ -329,8 +329,9 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const u
   const int g = w.h, nblk = w.j1 - w.j0, ks = w.j0 * BK, ke = w.j1 * BK;
   const bool real = R < rq.n * p.group;
   const int lim = real ? min(ke, kv4_row_limit(p, rq, R / p.group)) : ke;
-  // Q: the warp's 32 rows, copied along the rows; rows past the last are 0
-  {
+  // Q: the warp's 32 rows, copied along the rows; rows past the last are 0. A tile without keys needs none, and
+  // must not arrive: the issuer counts a phase of q_full for each work with keys and waits for every one.
+  if (nblk > 0) {
     const long src = real ? (long)(rq.q0 + R / p.group) * p.q_tok + (g * p.group + R % p.group) * p.q_head : -1;
 #pragma unroll 2
     for (int i = 0; i < CHUNKS; ++i) {
@@ -506,7 +507,10 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
   uint64_t* p_full = s_full + 4;     // [4]: P_t(j) is in its columns
   uint64_t* pv_done = p_full + 4;    // [4]: P_t V(j) completed
   uint64_t* s_read = pv_done + 4;    // [2]: the softmax has S_t(j) in registers (one buffer only)
-  uint64_t* q_full = s_read + 2;     // [2]: tile t's Q is in shared memory
+  // [2]: tile t's Q is in shared memory. One phase per work that has keys and rows in the tile, arrived on by the
+  // softmax's warps and waited for by the issuer; were one left out on either side, the wait of a later work would
+  // pass on an older phase's parity, and its scores would come from another work's Q.
+  uint64_t* q_full = s_read + 2;
   uint64_t* drain = q_full + 2;      // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [0] abort
@@ -585,10 +589,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     while (ok && walk.next(p, w)) {
       const int nblk = w.j1 - w.j0;
       live = t == 0 || w.rq.n * p.group - 256 * w.tile > 128;
-      if (nblk == 0) {
-        if (live && !w.rq.bad) ++loads;
-        continue;
-      }
+      if (nblk == 0) continue;   // no key in sight: there is nothing to multiply, and no Q to wait for
       ok = (!live || wait(&q_full[t], loads & 1)) && issue_s(0) && (!G::TWO || nblk == 1 || issue_s(1));
 #pragma unroll 1
       for (int j = 0; j < nblk && ok; ++j) {
