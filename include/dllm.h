@@ -303,7 +303,7 @@ int dllm_op_lm_head_conf_noalloc(const uint16_t* y, const uint16_t* head, int T,
  * no synchronisation, capturable in a CUDA graph. Nothing is kept between calls. Sizes are
  * checked on the host (DLLM_E_INVAL, nothing queued); what lies in device memory is checked
  * by the kernels, as each call says. Strides are in elements; the last dimension is
- * contiguous. */
+ * contiguous. Rows of an output that overlap one another (an expanded tensor) are refused. */
 #define DLLM_F32 0
 #define DLLM_BF16 1
 

@@ -58,6 +58,21 @@ bool vectors(const void* p, int type, long long tok, long long head) {
   return aligned16(p) && tok % per == 0 && head % per == 0;
 }
 
+// Whether the rows of an output [T][H][d] are apart: no element lies in two of them, i.e. no two rows i tokens
+// and j heads from one another start less than d elements apart. With the strides' signs dropped, j heads on are
+// the same as j back for some i.
+bool rows_apart(int T, int H, int d, long long tok, long long head) {
+  typedef __int128 wide;
+  const wide a = tok < 0 ? -(wide)tok : tok, b = head < 0 ? -(wide)head : head;
+  if ((T > 1 && a < d) || (H > 1 && b < d)) return false;
+  if (T <= 1 || H <= 1 || a >= b * (H - 1) + d || b >= a * (T - 1) + d) return true;   // one within the other
+  for (wide j = 1; j < H; ++j) {
+    const wide i = j * b / a, rest = j * b - i * a;   // the tokens next to head j's start
+    if ((i < T && rest < d) || (i + 1 < T && a - rest < d)) return false;
+  }
+  return true;
+}
+
 bool rope_ok(const dllm_rope* r, int head_dim) {
   return r->rotary_dim >= 2 && r->rotary_dim % 2 == 0 && r->rotary_dim <= 2 * DLLM_ROPE_MAX_PAIRS &&
          r->rotary_dim <= head_dim && (r->layout == DLLM_ROPE_HALF || r->layout == DLLM_ROPE_INTERLEAVED);
@@ -285,6 +300,7 @@ int dllm_op_rope(const dllm_rope* rope, const void* x, int x_type, long long x_t
   if (!x || !y || !pos) return DLLM_E_INVAL;
   if (x == y && (x_type != y_type || x_token_stride != y_token_stride || x_head_stride != y_head_stride))
     return DLLM_E_INVAL;
+  if (!rows_apart(T, H, head_dim, y_token_stride, y_head_stride)) return DLLM_E_INVAL;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const RopeParams r = rope_params(rope, transposed != 0);
   const bool vec = vectors(x, x_type, x_token_stride, x_head_stride) &&
@@ -344,6 +360,7 @@ int dllm_op_attn_kv4(const dllm_kv4* cache, const uint16_t* q, long long q_token
       !vectors(q, DLLM_BF16, q_token_stride, q_head_stride) ||
       !vectors(out, DLLM_BF16, out_token_stride, out_head_stride) || !aligned16(workspace))
     return DLLM_E_INVAL;
+  if (!rows_apart(T, H, cache->head_dim, out_token_stride, out_head_stride)) return DLLM_E_INVAL;
   const int group = H / cache->n_kv_heads;
   const AttnPlan a = attn_plan(B, T, max_q, max_kv, group, cache->n_kv_heads, cache->head_dim);
   // the few-row kernel's grid; the tensor-core kernel's sums

@@ -1,0 +1,54 @@
+"""Calls on rotary positions and the paged 4-bit KV cache that other tests do not make: which tensors are taken and
+which are refused, on the GPU."""
+
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+from masked_block_diffusion_b200 import DllmError, KVCache4, Rope, binding, build, rope
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build_all()
+    binding.load()
+
+
+def i32(v):
+    return torch.tensor(np.asarray(v, np.int32), device="cuda")
+
+
+@pytest.mark.parametrize("T,H,d", [(2, 2, 4), (3, 4, 6), (5, 2, 2), (1, 3, 4), (3, 1, 4)])
+def test_rope_takes_outputs_of_any_strides_whose_rows_are_apart(T, H, d):
+    x, pos, plan = torch.randn(T, H, d, device="cuda"), i32(range(T)), Rope(2)
+    want = rope(x, pos, plan)
+    for tok, head in itertools.product(range(0, 14), repeat=2):
+        room = torch.full((T * tok + H * head + d,), 7.0, device="cuda")
+        out = room.as_strided((T, H, d), (tok, head, 1))
+        cells = {t * tok + h * head + e for t in range(T) for h in range(H) for e in range(d)}
+        if len(cells) < T * H * d:
+            with pytest.raises(DllmError):
+                rope(x, pos, plan, out=out)
+            assert (room == 7.0).all()
+        else:
+            rope(x, pos, plan, out=out)
+            assert torch.equal(out, want), (tok, head)
+
+
+@pytest.mark.parametrize("queries", [1, 40])
+def test_attend_refuses_an_expanded_output_and_takes_heads_first(queries):
+    cache = KVCache4(4, 32, 2, 64)
+    q = torch.randn(queries, 4, 64, device="cuda").bfloat16()
+    args = (i32([0, queries]), i32([70]), i32([[2, 0, 1]]), queries, 70)
+    want = cache.attend(q, *args)
+    for shape in ((queries, 1, 64), (1, 4, 64)):
+        if queries == 1 and shape[0] == 1:
+            continue
+        with pytest.raises(DllmError):
+            cache.attend(q, *args, out=torch.zeros(shape, dtype=torch.bfloat16, device="cuda").expand(queries, 4, 64))
+    turned = torch.zeros(4, queries, 64, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    assert torch.equal(cache.attend(q, *args, out=turned), want)

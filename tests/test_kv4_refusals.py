@@ -1,0 +1,29 @@
+"""Calls on rotary positions and the paged 4-bit KV cache that are refused before anything is queued (no GPU)."""
+
+import pytest
+
+from masked_block_diffusion_b200 import Rope, binding, build
+
+P = 1 << 24      # stands for a device address: a refused call never reads it
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build_dllm()
+    return binding.load()
+
+
+def call_rope(lib, T=4, H=2, d=64, tok=128, head=64, y=2 * P, x=P, x_type=0, y_type=0, x_tok=128, x_head=64):
+    return lib.dllm_op_rope(Rope(2).c, x, x_type, x_tok, x_head, P, T, H, d, y, y_type, tok, head, 0, None)
+
+
+def call_attend(lib, T=4, H=2, tok=128, head=64, out=2 * P, q=P, q_tok=128, q_head=64):
+    c = binding.dllm_kv4(P, P, 8, 64, 2, 64)
+    return lib.dllm_op_attn_kv4(c, q, q_tok, q_head, out, tok, head, None, P, P, 1, T, 1, 64, H, P, 1, 0, 0.125, None, 0, None)
+
+
+@pytest.mark.parametrize("tok,head", [(0, 64), (128, 0), (0, 0), (64, 64), (120, 64), (128, 56), (-64, 64), (96, 192), (64, 96)])
+def test_outputs_whose_rows_overlap_are_refused(lib, tok, head):
+    assert call_rope(lib, tok=tok, head=head) == binding.DLLM_E_INVAL
+    if tok % 8 == 0 and head % 8 == 0:
+        assert call_attend(lib, tok=tok, head=head) == binding.DLLM_E_INVAL
