@@ -303,7 +303,9 @@ int dllm_op_lm_head_conf_noalloc(const uint16_t* y, const uint16_t* head, int T,
  * no synchronisation, capturable in a CUDA graph. Nothing is kept between calls. Sizes are
  * checked on the host (DLLM_E_INVAL, nothing queued); what lies in device memory is checked
  * by the kernels, as each call says. Strides are in elements; the last dimension is
- * contiguous. Rows of an output that overlap one another (an expanded tensor) are refused. */
+ * contiguous. Rows of an output that overlap one another (an expanded tensor) are refused; so are
+ * an output and an input, or two outputs, that share memory otherwise than as a call allows, where
+ * both are without gaps (with gaps it is the caller's to keep them apart). */
 #define DLLM_F32 0
 #define DLLM_BF16 1
 
@@ -395,7 +397,8 @@ int dllm_op_read_kv4(const dllm_kv4* cache, const int32_t* req, const int32_t* p
  *   row that sees no key: it joins this result with attention over other keys.
  * Rows of q that no request covers are left as they were in out and lse. max_q and max_kv are the
  * caller's bounds on the requests' queries and keys (max_q <= T, max_kv < 2^29; nothing is
- * queued if max_q or B is 0). out may be q itself, with equal strides. A request that
+ * queued if max_q or B is 0). out may be q itself, with equal strides; other overlaps are not
+ * allowed. A request that
  * exceeds them or its row of the table, or with kv_len < 0, gets NaN in all its rows; one whose
  * q_start range is not within 0 .. T is skipped; a page id outside the cache gives NaN in the
  * rows that see it (other rows of that request may be NaN too), as does a kernel that gives

@@ -73,6 +73,16 @@ bool rows_apart(int T, int H, int d, long long tok, long long head) {
   return true;
 }
 
+// Whether two gapless tensors [T][H][d] share memory. (Of tensors with gaps, slices of one buffer for instance,
+// the ranges may cross although no element is in both; those are the caller's to keep apart.)
+bool share_memory(const void* x, size_t x_bytes, const void* y, size_t y_bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return a < b + y_bytes && b < a + x_bytes;
+}
+bool gapless(int T, int H, int d, long long tok, long long head) {
+  return (T <= 1 || tok == (long long)H * d) && (H <= 1 || head == d);
+}
+
 bool rope_ok(const dllm_rope* r, int head_dim) {
   return r->rotary_dim >= 2 && r->rotary_dim % 2 == 0 && r->rotary_dim <= 2 * DLLM_ROPE_MAX_PAIRS &&
          r->rotary_dim <= head_dim && (r->layout == DLLM_ROPE_HALF || r->layout == DLLM_ROPE_INTERLEAVED);
@@ -301,6 +311,10 @@ int dllm_op_rope(const dllm_rope* rope, const void* x, int x_type, long long x_t
   if (x == y && (x_type != y_type || x_token_stride != y_token_stride || x_head_stride != y_head_stride))
     return DLLM_E_INVAL;
   if (!rows_apart(T, H, head_dim, y_token_stride, y_head_stride)) return DLLM_E_INVAL;
+  const size_t n = (size_t)T * H * head_dim;
+  if (x != y && gapless(T, H, head_dim, x_token_stride, x_head_stride) &&
+      gapless(T, H, head_dim, y_token_stride, y_head_stride) && share_memory(x, n * size_of(x_type), y, n * size_of(y_type)))
+    return DLLM_E_INVAL;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const RopeParams r = rope_params(rope, transposed != 0);
   const bool vec = vectors(x, x_type, x_token_stride, x_head_stride) &&
@@ -332,6 +346,8 @@ int dllm_op_read_kv4(const dllm_kv4* cache, const int32_t* req, const int32_t* p
                      int n_req, int table_stride, uint16_t* k_out, uint16_t* v_out, int zero_padding, void* stream) {
   if (!cache_ok(cache) || T < 0 || !aligned16(k_out) || !aligned16(v_out)) return DLLM_E_INVAL;
   if (T == 0 || (!k_out && !v_out)) return DLLM_OK;
+  const size_t bytes = (size_t)T * cache->n_kv_heads * cache->head_dim * 2;
+  if (k_out && v_out && share_memory(k_out, bytes, v_out, bytes)) return DLLM_E_INVAL;
   if (!addr_ok(req, pos, table, n_req, table_stride)) return DLLM_E_INVAL;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const Kv4Addr a{req, pos, table, n_req, table_stride};
@@ -361,6 +377,11 @@ int dllm_op_attn_kv4(const dllm_kv4* cache, const uint16_t* q, long long q_token
       !vectors(out, DLLM_BF16, out_token_stride, out_head_stride) || !aligned16(workspace))
     return DLLM_E_INVAL;
   if (!rows_apart(T, H, cache->head_dim, out_token_stride, out_head_stride)) return DLLM_E_INVAL;
+  if (q == out ? (T > 1 && q_token_stride != out_token_stride) || (H > 1 && q_head_stride != out_head_stride)
+               : gapless(T, H, cache->head_dim, q_token_stride, q_head_stride) &&
+                     gapless(T, H, cache->head_dim, out_token_stride, out_head_stride) &&
+                     share_memory(q, (size_t)T * H * cache->head_dim * 2, out, (size_t)T * H * cache->head_dim * 2))
+    return DLLM_E_INVAL;
   const int group = H / cache->n_kv_heads;
   const AttnPlan a = attn_plan(B, T, max_q, max_kv, group, cache->n_kv_heads, cache->head_dim);
   // the few-row kernel's grid; the tensor-core kernel's sums

@@ -52,3 +52,31 @@ def test_attend_refuses_an_expanded_output_and_takes_heads_first(queries):
             cache.attend(q, *args, out=torch.zeros(shape, dtype=torch.bfloat16, device="cuda").expand(queries, 4, 64))
     turned = torch.zeros(4, queries, 64, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
     assert torch.equal(cache.attend(q, *args, out=turned), want)
+
+
+@pytest.mark.parametrize("queries", [1, 40])
+def test_slices_of_one_buffer_are_taken_and_shifted_views_are_not(queries):
+    cache = KVCache4(4, 32, 2, 64)
+    cache.codes.random_(0, 256)
+    cache.scales.fill_(100)
+    args = (i32([0, queries]), i32([70]), i32([[2, 0, 1]]), queries, 70)
+    buf = torch.randn(queries, 12, 64, device="cuda").bfloat16()
+    want = cache.attend(buf[:, 4:8].contiguous(), *args)
+    assert torch.equal(cache.attend(buf[:, 4:8], *args, out=buf[:, 8:]), want)    # side by side
+    assert torch.equal(cache.attend(buf[:, 4:8], *args, out=buf[:, 4:8]), want)   # in place
+    flat = torch.randn((queries + 1) * 256, device="cuda").bfloat16()
+    q, shifted = flat[:-256].view(queries, 4, 64), flat[64:64 - 256].view(queries, 4, 64)
+    with pytest.raises(DllmError):
+        cache.attend(q, *args, out=shifted)
+    pos = i32(range(queries))
+    with pytest.raises(DllmError):
+        rope(q, pos, Rope(64), out=shifted)
+    req, pos, table = i32([0] * 5), i32(range(5)), i32([[2, 0, 1]])
+    both = torch.zeros(7, 2, 64, dtype=torch.bfloat16, device="cuda")
+    for k, v in ((both[:5], both[:5]), (both[:5], both[2:])):
+        with pytest.raises(DllmError):
+            cache.read(req, pos, table, k_out=k, v_out=v)
+    assert not both.any()
+    pair = torch.zeros(2, 5, 2, 64, dtype=torch.bfloat16, device="cuda")          # next to each other
+    cache.read(req, pos, table, k_out=pair[0], v_out=pair[1])
+    assert all(torch.equal(a, b) for a, b in zip(pair, cache.read(req, pos, table)))

@@ -27,3 +27,25 @@ def test_outputs_whose_rows_overlap_are_refused(lib, tok, head):
     assert call_rope(lib, tok=tok, head=head) == binding.DLLM_E_INVAL
     if tok % 8 == 0 and head % 8 == 0:
         assert call_attend(lib, tok=tok, head=head) == binding.DLLM_E_INVAL
+
+
+def test_outputs_that_share_memory_with_an_input_are_refused(lib):
+    n = 4 * 2 * 64
+    for off in (4, 64 * 4, n * 4 - 4):                               # x fp32, y fp32, ahead and behind
+        assert call_rope(lib, y=P + off) == binding.DLLM_E_INVAL
+        assert call_rope(lib, x=P + off, y=P) == binding.DLLM_E_INVAL
+    assert call_rope(lib, x_type=1, y=P + n * 2 - 4) == binding.DLLM_E_INVAL
+    assert call_rope(lib, x_type=1, x=P + n * 4 - 2, y=P) == binding.DLLM_E_INVAL
+    assert call_rope(lib, T=1, tok=0, x_tok=7, y=P + 8) == binding.DLLM_E_INVAL
+    for off in (16, 256, n * 2 - 16):
+        assert call_attend(lib, out=P + off) == binding.DLLM_E_INVAL
+        assert call_attend(lib, q=P + off, out=P) == binding.DLLM_E_INVAL
+    assert call_attend(lib, out=P, tok=256) == binding.DLLM_E_INVAL    # q itself, with other strides
+    assert call_attend(lib, out=P, tok=64, head=256) == binding.DLLM_E_INVAL
+
+
+def test_reading_keys_and_values_into_one_place_is_refused(lib):
+    c = binding.dllm_kv4(P, P, 8, 64, 2, 64)
+    n = 3 * 2 * 64 * 2
+    for k, v in ((P, P), (P, P + n - 16), (P + n - 16, P)):
+        assert lib.dllm_op_read_kv4(c, P, P, 3, P, 1, 1, k, v, 0, None) == binding.DLLM_E_INVAL
