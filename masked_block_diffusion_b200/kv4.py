@@ -17,6 +17,7 @@ import contextlib
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding
 
@@ -98,6 +99,13 @@ def _refuse_grad() -> None:
                            "(rope(..., transposed=True) is the gradient of rope)")
 
 
+def _refuse_tangent(*tensors: torch.Tensor) -> None:
+    """Inside a forward_ad level: none of the tensors may be a dual one. (Such a tensor does not say so by requires_grad.)"""
+    if any(forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise RuntimeError("these operations carry no tangent: call them on primals (rope is linear: rope of the "
+                           "tangent is the result's tangent)")
+
+
 _HERE = contextlib.nullcontext()
 
 
@@ -139,6 +147,8 @@ def rope(x: torch.Tensor, pos: torch.Tensor, plan: Rope, out: Optional[torch.Ten
         yt, yh = _heads("out", out, dev, T, H, hd, _TYPES)
     if x.requires_grad:
         _refuse_grad()
+    if forward_ad._current_level >= 0:   # (a look at a number, where asking each tensor costs 0.3 us)
+        _refuse_tangent(x, out)
     with _on(dev):
         binding.dllm_op_rope(plan.c, x.data_ptr(), _TYPES[x.dtype], xt, xh, at, T, H, hd, out.data_ptr(),
                              _TYPES[out.dtype], yt, yh, 1 if transposed else 0, _stream_of(dev))
@@ -199,6 +209,8 @@ class KVCache4:
         vt, vh = _heads("v", v, dev, T, H, d, (k.dtype,))
         if k.requires_grad or v.requires_grad:
             _refuse_grad()
+        if forward_ad._current_level >= 0:
+            _refuse_tangent(k, v)
         req_ptr, pos_ptr = _ints("req", req, dev, T), _ints("pos", pos, dev, T)
         rope_ptr = None if rope_pos is None else _ints("rope_pos", rope_pos, dev, T)
         tab, rows, stride = _table(table, dev)
@@ -223,6 +235,8 @@ class KVCache4:
                 if not t.is_contiguous():
                     _bad(name, "has to be contiguous")
             outs.append(t)
+        if forward_ad._current_level >= 0:
+            _refuse_tangent(*outs)
         req_ptr, pos_ptr = _ints("req", req, dev, T), _ints("pos", pos, dev, T)
         tab, rows, stride = _table(table, dev)
         with _on(dev):
@@ -256,6 +270,8 @@ class KVCache4:
             ot, oh = H * hd, hd
         else:
             ot, oh = _heads("out", out, dev, T, H, hd, (torch.bfloat16,))
+        if forward_ad._current_level >= 0:
+            _refuse_tangent(q, out)
         lse = q.new_empty((T, H), dtype=torch.float32) if return_lse else None
         if workspace is None:
             size = self.workspace_bytes(B, T, max_q, max_kv, H)

@@ -80,3 +80,30 @@ def test_slices_of_one_buffer_are_taken_and_shifted_views_are_not(queries):
     pair = torch.zeros(2, 5, 2, 64, dtype=torch.bfloat16, device="cuda")          # next to each other
     cache.read(req, pos, table, k_out=pair[0], v_out=pair[1])
     assert all(torch.equal(a, b) for a, b in zip(pair, cache.read(req, pos, table)))
+
+
+def _dual(t):
+    return torch.autograd.forward_ad.make_dual(t, torch.ones_like(t))
+
+
+def test_dual_tensors_are_refused_and_plain_ones_within_their_level_are_not():
+    cache, plan = KVCache4(4, 32, 2, 64), Rope(64)
+    x, pos, req, table = torch.randn(3, 2, 64, device="cuda"), i32(range(3)), i32([0] * 3), i32([[2, 0, 1]])
+    q = torch.randn(3, 4, 64, device="cuda").bfloat16()
+    args = (i32([0, 3]), i32([3]), table, 3, 3)
+    held = torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    with torch.autograd.forward_ad.dual_level(), torch.no_grad():
+        for bad in (lambda: rope(_dual(x), pos, plan), lambda: rope(x, pos, plan, out=_dual(x.clone())),
+                    lambda: cache.append(_dual(x), x, req, pos, table), lambda: cache.append(x, _dual(x), req, pos, table),
+                    lambda: cache.read(req, pos, table, k_out=held[0], v_out=_dual(held[1])),
+                    lambda: cache.attend(_dual(q), *args), lambda: cache.attend(q, *args, out=_dual(q.clone()))):
+            with pytest.raises(RuntimeError, match="tangent"):
+                bad()
+        assert not cache.codes.any()
+        # the way that the message names
+        dual = _dual(x)
+        y, dy = (rope(t, pos, plan) for t in torch.autograd.forward_ad.unpack_dual(dual))
+        cache.append(x, x, req, pos, table)
+        cache.read(req, pos, table)
+        cache.attend(q, *args)
+    assert torch.equal(y, rope(x, pos, plan)) and torch.equal(dy, rope(torch.ones_like(x), pos, plan))

@@ -49,3 +49,16 @@ def test_reading_keys_and_values_into_one_place_is_refused(lib):
     n = 3 * 2 * 64 * 2
     for k, v in ((P, P), (P, P + n - 16), (P + n - 16, P)):
         assert lib.dllm_op_read_kv4(c, P, P, 3, P, 1, 1, k, v, 0, None) == binding.DLLM_E_INVAL
+
+
+def test_tangents_are_seen_where_requires_grad_is_not_set():
+    torch = pytest.importorskip("torch")
+    from masked_block_diffusion_b200 import kv4
+    x = torch.ones(3)
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(x, x)
+        assert torch.autograd.forward_ad._current_level >= 0 and not dual.requires_grad
+        with pytest.raises(RuntimeError):
+            kv4._refuse_tangent(x, dual)
+        kv4._refuse_tangent(x, x)
+    assert torch.autograd.forward_ad._current_level < 0
