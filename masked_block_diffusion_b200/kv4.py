@@ -234,6 +234,8 @@ class KVCache4:
                 _heads(name, t, dev, T, H, d, (torch.bfloat16,))
                 if not t.is_contiguous():
                     _bad(name, "has to be contiguous")
+                if t.requires_grad:
+                    _refuse_grad()
             outs.append(t)
         if forward_ad._current_level >= 0:
             _refuse_tangent(*outs)
@@ -270,6 +272,8 @@ class KVCache4:
             ot, oh = H * hd, hd
         else:
             ot, oh = _heads("out", out, dev, T, H, hd, (torch.bfloat16,))
+            if out.requires_grad:
+                _refuse_grad()
         if forward_ad._current_level >= 0:
             _refuse_tangent(q, out)
         lse = q.new_empty((T, H), dtype=torch.float32) if return_lse else None

@@ -107,3 +107,23 @@ def test_dual_tensors_are_refused_and_plain_ones_within_their_level_are_not():
         cache.read(req, pos, table)
         cache.attend(q, *args)
     assert torch.equal(y, rope(x, pos, plan)) and torch.equal(dy, rope(torch.ones_like(x), pos, plan))
+
+
+def test_outputs_that_require_a_gradient_are_refused():
+    """As torch refuses to write to them in place; without gradients being recorded both may."""
+    cache, plan = KVCache4(4, 32, 2, 64), Rope(64)
+    x, pos, req, table = torch.randn(3, 2, 64, device="cuda"), i32(range(3)), i32([0] * 3), i32([[2, 0, 1]])
+    q = torch.randn(3, 4, 64, device="cuda").bfloat16()
+    args = (i32([0, 3]), i32([3]), table, 3, 3)
+    leaf = [torch.full(t.shape, 5.0, dtype=t.dtype, device="cuda", requires_grad=True) for t in (x, q, x.bfloat16(), x.bfloat16())]
+    plain = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    calls = (lambda: rope(x, pos, plan, out=leaf[0]), lambda: cache.attend(q, *args, out=leaf[1]),
+             lambda: cache.read(req, pos, table, k_out=leaf[2], v_out=plain), lambda: cache.read(req, pos, table, k_out=plain, v_out=leaf[3]))
+    for call in calls:
+        with pytest.raises(RuntimeError, match="gradient"):
+            call()
+    assert all((t == 5.0).all() for t in leaf)
+    with torch.no_grad():
+        for call in calls:
+            call()
+    assert not any((t == 5.0).any() for t in leaf)
