@@ -8,7 +8,8 @@ behind it (include/dllm.h) says what each call computes and how it treats paddin
 ids and bad lengths.
 
 Tensors are those of the call's stream: as with any torch operation, the caller orders other
-streams' work on them.
+streams' work on them. A write to a tensor that the caller gave counts as one in place: a
+backward pass that had saved the old values raises.
 """
 
 from __future__ import annotations
@@ -18,6 +19,7 @@ from typing import Optional, Tuple
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import binding
 
@@ -133,7 +135,8 @@ def rope(x: torch.Tensor, pos: torch.Tensor, plan: Rope, out: Optional[torch.Ten
     T, H, hd = x.shape
     xt, xh = _heads("x", x, dev, T, H, hd, _TYPES)
     at = _ints("pos", pos, dev, T)
-    if out is None:
+    given = out is not None
+    if not given:
         dtype = out_dtype or x.dtype
         if dtype not in _TYPES:
             _bad("out_dtype", f"{dtype}, expected one of {[str(d) for d in _TYPES]}")
@@ -152,6 +155,8 @@ def rope(x: torch.Tensor, pos: torch.Tensor, plan: Rope, out: Optional[torch.Ten
     with _on(dev):
         binding.dllm_op_rope(plan.c, x.data_ptr(), _TYPES[x.dtype], xt, xh, at, T, H, hd, out.data_ptr(),
                              _TYPES[out.dtype], yt, yh, 1 if transposed else 0, _stream_of(dev))
+    if given:
+        increment_version(out)
     return out
 
 
@@ -244,6 +249,8 @@ class KVCache4:
         with _on(dev):
             binding.dllm_op_read_kv4(self.c, req_ptr, pos_ptr, T, tab, rows, stride, outs[0].data_ptr(),
                                      outs[1].data_ptr(), 1 if made else 0, _stream_of(dev))
+        if not made:
+            increment_version(outs)
         return outs[0], outs[1]
 
     def attend(self, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor, max_q: int,
@@ -267,7 +274,8 @@ class KVCache4:
         tab, rows, stride = _table(table, dev)
         if rows < B:
             _bad("table", f"{rows} rows for {B} requests")
-        if out is None:
+        given = out is not None
+        if not given:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
             ot, oh = H * hd, hd
         else:
@@ -291,6 +299,8 @@ class KVCache4:
                                      lse.data_ptr() if return_lse else None, start_ptr, len_ptr, B, T, max_q, max_kv, H,
                                      tab, stride, 1 if causal else 0, hd ** -0.5 if scale is None else scale,
                                      None if workspace is None else workspace.data_ptr(), size, _stream_of(dev))
+        if given:
+            increment_version(out)
         return (out, lse) if return_lse else out
 
     def workspace_bytes(self, B: int, T: int, max_q: int, max_kv: int, heads: int) -> int:

@@ -127,3 +127,23 @@ def test_outputs_that_require_a_gradient_are_refused():
         for call in calls:
             call()
     assert not any((t == 5.0).any() for t in leaf)
+
+
+def test_a_backward_pass_notices_that_a_saved_tensor_was_written_to():
+    cache, plan = KVCache4(4, 32, 2, 64), Rope(64)
+    pos, req, table = i32(range(3)), i32([0] * 3), i32([[2, 0, 1]])
+    args = (i32([0, 3]), i32([3]), table, 3, 3)
+    spare = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    x, q = (torch.randn(3, h, 64, device="cuda").bfloat16() for h in (2, 4))
+    for shape, write in ((x, lambda y: rope(x, pos, plan, out=y)), (x, lambda y: rope(y, pos, plan, out=y)),
+                         (q, lambda y: cache.attend(q, *args, out=y)), (x, lambda y: cache.read(req, pos, table, k_out=y, v_out=spare)),
+                         (x, lambda y: cache.read(req, pos, table, k_out=spare, v_out=y))):
+        leaf = torch.randn_like(shape).requires_grad_()
+        y = leaf.exp()                                               # its gradient is made of y itself
+        write(y.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+    with torch.inference_mode():                                     # where nothing counts writes
+        y = torch.empty_like(x)
+        assert rope(x, pos, plan, out=y) is y
+        cache.read(req, pos, table, k_out=y, v_out=torch.empty_like(y))
