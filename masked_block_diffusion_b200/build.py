@@ -58,7 +58,8 @@ def build_dllm(force: bool = False, verbose_ptxas: bool = False) -> str:
         if p.wait() != 0:
             raise subprocess.CalledProcessError(p.returncode, cmd)
         os.replace(obj + ".tmp", obj)
-    if running or not os.path.exists(LIB):
+    # an object file may be newer than the library without a unit compiled here: the last link did not finish
+    if running or _stale(LIB, [o for o in objs if os.path.exists(o)]):
         missing = [o for o in objs if not os.path.exists(o)]
         if missing:
             return build_dllm(True, verbose_ptxas)
