@@ -54,10 +54,14 @@ def build_dllm(force: bool = False, verbose_ptxas: bool = False) -> str:
         if verbose_ptxas:
             cmd.insert(1, "-Xptxas=-v")
         running.append((subprocess.Popen(cmd), cmd, obj))
-    for p, cmd, obj in running:
-        if p.wait() != 0:
-            raise subprocess.CalledProcessError(p.returncode, cmd)
-        os.replace(obj + ".tmp", obj)
+    failed = None
+    for p, cmd, obj in running:   # all of them, so that none still writes its file when a later build begins
+        if p.wait() == 0:
+            os.replace(obj + ".tmp", obj)
+        elif failed is None:
+            failed = subprocess.CalledProcessError(p.returncode, cmd)
+    if failed is not None:
+        raise failed
     # an object file may be newer than the library without a unit compiled here: the last link did not finish
     if running or _stale(LIB, [o for o in objs if os.path.exists(o)]):
         missing = [o for o in objs if not os.path.exists(o)]

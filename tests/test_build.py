@@ -74,6 +74,19 @@ def test_a_link_that_failed_is_made_up_for(tree, monkeypatch):
     assert (tree / "lib.so").read_text() == "a2 b1 "
 
 
+def test_a_unit_that_fails_does_not_leave_the_other_ones_compiler_behind(tree, monkeypatch):
+    monkeypatch.setenv("FAKE_FAIL", "a.o")
+    monkeypatch.setenv("FAKE_SLOW", "b.o")
+    with pytest.raises(subprocess.CalledProcessError):
+        build.build_dllm()
+    assert "end b.o.tmp" in (tree / "log").read_text()
+    assert (tree / "obj" / "b.o").exists() and not (tree / "lib.so").exists()
+    monkeypatch.setenv("FAKE_FAIL", "none")
+    build.build_dllm()
+    assert (tree / "lib.so").read_text() == "a1 b1 "
+    assert (tree / "log").read_text().count("start b.o") == 1            # what compiled is kept
+
+
 def test_nothing_is_done_where_nothing_changed(tree):
     build.build_dllm()
     log = (tree / "log").read_text()
