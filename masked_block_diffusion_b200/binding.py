@@ -302,7 +302,12 @@ def dllm_op_quantize_fp8(w_ptr, rows, cols, q_ptr, exps_ptr, stream_ptr):
            "dllm_op_quantize_fp8")
 
 
+_INT_MAX = 0x7FFFFFFF   # ctypes drops the upper bits of what an int does not hold, so sizes are looked at first
+
+
 def dllm_rope_init(rotary_dim, layout, theta, scaling, factor, original_ctx, beta_fast, beta_slow) -> dllm_rope:
+    if abs(rotary_dim) > _INT_MAX:
+        _check(DLLM_E_INVAL, "dllm_rope_init")
     r = dllm_rope()
     _check(load().dllm_rope_init(ctypes.byref(r), rotary_dim, layout, theta, scaling, factor, original_ctx, beta_fast,
                                  beta_slow), "dllm_rope_init")
@@ -313,6 +318,8 @@ def dllm_rope_init(rotary_dim, layout, theta, scaling, factor, original_ctx, bet
 
 def dllm_op_rope(rope: dllm_rope, x_ptr, x_type, x_token_stride, x_head_stride, pos_ptr, T, H, head_dim, y_ptr, y_type,
                  y_token_stride, y_head_stride, transposed, stream_ptr):
+    if not 0 <= T | H | head_dim <= _INT_MAX:
+        _check(DLLM_E_INVAL, "dllm_op_rope")
     code = (_lib or load()).dllm_op_rope(rope, x_ptr, x_type, x_token_stride, x_head_stride, pos_ptr, T, H, head_dim,
                                          y_ptr, y_type, y_token_stride, y_head_stride, transposed, stream_ptr)
     if code:
@@ -322,6 +329,8 @@ def dllm_op_rope(rope: dllm_rope, x_ptr, x_type, x_token_stride, x_head_stride, 
 def dllm_op_append_kv4(cache: dllm_kv4, k_ptr, k_token_stride, k_head_stride, v_ptr, v_token_stride, v_head_stride, type_,
                        req_ptr, pos_ptr, rope_pos_ptr, T, table_ptr, n_req, table_stride, rope, stream_ptr):
     """rope: a dllm_rope or None; rope_pos_ptr 0: pos."""
+    if not 0 <= T | n_req | table_stride <= _INT_MAX:
+        _check(DLLM_E_INVAL, "dllm_op_append_kv4")
     code = (_lib or load()).dllm_op_append_kv4(cache, k_ptr, k_token_stride, k_head_stride, v_ptr, v_token_stride,
                                                v_head_stride, type_, req_ptr, pos_ptr, rope_pos_ptr, T, table_ptr,
                                                n_req, table_stride, rope, stream_ptr)
@@ -331,6 +340,8 @@ def dllm_op_append_kv4(cache: dllm_kv4, k_ptr, k_token_stride, k_head_stride, v_
 
 def dllm_op_read_kv4(cache: dllm_kv4, req_ptr, pos_ptr, T, table_ptr, n_req, table_stride, k_out_ptr, v_out_ptr,
                      zero_padding, stream_ptr):
+    if not 0 <= T | n_req | table_stride <= _INT_MAX:
+        _check(DLLM_E_INVAL, "dllm_op_read_kv4")
     code = (_lib or load()).dllm_op_read_kv4(cache, req_ptr, pos_ptr, T, table_ptr, n_req, table_stride, k_out_ptr,
                                              v_out_ptr, zero_padding, stream_ptr)
     if code:
@@ -340,6 +351,8 @@ def dllm_op_read_kv4(cache: dllm_kv4, req_ptr, pos_ptr, T, table_ptr, n_req, tab
 def dllm_op_attn_kv4(cache: dllm_kv4, q_ptr, q_token_stride, q_head_stride, out_ptr, out_token_stride, out_head_stride,
                      lse_ptr, q_start_ptr, kv_len_ptr, B, T, max_q, max_kv, H, table_ptr, table_stride, causal, scale,
                      workspace_ptr, workspace_bytes, stream_ptr):
+    if not 0 <= B | T | max_q | max_kv | H | table_stride <= _INT_MAX:
+        _check(DLLM_E_INVAL, "dllm_op_attn_kv4")
     code = (_lib or load()).dllm_op_attn_kv4(cache, q_ptr, q_token_stride, q_head_stride, out_ptr, out_token_stride,
                                              out_head_stride, lse_ptr, q_start_ptr, kv_len_ptr, B, T, max_q, max_kv,
                                              H, table_ptr, table_stride, causal, scale, workspace_ptr,
@@ -349,6 +362,8 @@ def dllm_op_attn_kv4(cache: dllm_kv4, q_ptr, q_token_stride, q_head_stride, out_
 
 
 def dllm_op_attn_kv4_workspace(cache: dllm_kv4, B, T, max_q, max_kv, H) -> int:
+    if not 0 <= B | T | max_q | max_kv | H <= _INT_MAX:
+        _check(DLLM_E_INVAL, "dllm_op_attn_kv4_workspace")
     n = (_lib or load()).dllm_op_attn_kv4_workspace(cache, B, T, max_q, max_kv, H)
     if n < 0:
         _check(n, "dllm_op_attn_kv4_workspace")

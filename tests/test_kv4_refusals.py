@@ -62,3 +62,31 @@ def test_tangents_are_seen_where_requires_grad_is_not_set():
             kv4._refuse_tangent(x, dual)
         kv4._refuse_tangent(x, x)
     assert torch.autograd.forward_ad._current_level < 0
+
+
+WIDE = 1 << 32                                                       # an int of 32 bits would take this as 0
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """Not taken modulo 2^32 on their way to the library."""
+    c, plan = binding.dllm_kv4(P, P, 8, 64, 2, 64), Rope(64).c
+    rope = dict(T=4, H=2, head_dim=64)
+    page = dict(T=4, n_req=1, table_stride=1)
+    attn = dict(B=1, T=4, max_q=1, max_kv=64, H=2)
+    calls = [(binding.dllm_op_rope, rope, lambda a: (plan, P, 0, 128, 64, P, a["T"], a["H"], a["head_dim"], 2 * P, 0, 128, 64, 0, None)),
+             (binding.dllm_op_append_kv4, page, lambda a: (c, P, 128, 64, P, 128, 64, 0, P, P, None, a["T"], P, a["n_req"], a["table_stride"],
+                                                           None, None)),
+             (binding.dllm_op_read_kv4, page, lambda a: (c, P, P, a["T"], P, a["n_req"], a["table_stride"], P, 2 * P, 0, None)),
+             (binding.dllm_op_attn_kv4, {**attn, "table_stride": 1},
+              lambda a: (c, P, 128, 64, 2 * P, 128, 64, None, P, P, a["B"], a["T"], a["max_q"], a["max_kv"], a["H"], P, a["table_stride"],
+                         0, 0.125, None, 0, None)),
+             (binding.dllm_op_attn_kv4_workspace, attn, lambda a: (c, a["B"], a["T"], a["max_q"], a["max_kv"], a["H"]))]
+    for f, sizes, args in calls:
+        for name in sizes:
+            for off in (WIDE, -WIDE if name in ("T", "B") else WIDE * 3):
+                with pytest.raises(binding.DllmError) as e:
+                    f(*args({**sizes, name: sizes[name] * (off > 0) + off}))
+                assert e.value.code == binding.DLLM_E_INVAL, (f.__name__, name)
+    for n in (WIDE + 64, 64 - WIDE):
+        with pytest.raises(binding.DllmError):
+            Rope(n)
