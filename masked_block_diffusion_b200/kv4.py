@@ -85,12 +85,12 @@ def _ints(name: str, t: torch.Tensor, dev: int, n: int) -> int:
     return t.data_ptr()
 
 
-def _table(t: torch.Tensor, dev: int) -> tuple:
-    """(address, rows, columns)"""
+def _table(t: torch.Tensor, dev: int, n: int) -> tuple:
+    """(address, rows, columns) of the table of n requests or tokens; it may be empty if there are none."""
     if t.dtype is not torch.int32 or t.dim() != 2 or t.get_device() != dev:
         _bad("table", f"expected int32 [requests][pages] on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     rows, cols = t.shape
-    if rows < 1 or cols < 1 or not t.is_contiguous():   # (a slice's row stride would be taken for its width)
+    if (n > 0 and (rows < 1 or cols < 1)) or not t.is_contiguous():   # (a slice's row stride would be taken for its width)
         _bad("table", f"expected a contiguous tensor of at least one row and page, got {tuple(t.shape)}")
     return t.data_ptr(), rows, cols
 
@@ -218,7 +218,7 @@ class KVCache4:
             _refuse_tangent(k, v)
         req_ptr, pos_ptr = _ints("req", req, dev, T), _ints("pos", pos, dev, T)
         rope_ptr = None if rope_pos is None else _ints("rope_pos", rope_pos, dev, T)
-        tab, rows, stride = _table(table, dev)
+        tab, rows, stride = _table(table, dev, T)
         with _on(dev):
             binding.dllm_op_append_kv4(self.c, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _TYPES[k.dtype], req_ptr,
                                        pos_ptr, rope_ptr, T, tab, rows, stride, None if rope is None else rope.c,
@@ -245,7 +245,7 @@ class KVCache4:
         if forward_ad._current_level >= 0:
             _refuse_tangent(*outs)
         req_ptr, pos_ptr = _ints("req", req, dev, T), _ints("pos", pos, dev, T)
-        tab, rows, stride = _table(table, dev)
+        tab, rows, stride = _table(table, dev, T)
         with _on(dev):
             binding.dllm_op_read_kv4(self.c, req_ptr, pos_ptr, T, tab, rows, stride, outs[0].data_ptr(),
                                      outs[1].data_ptr(), 1 if made else 0, _stream_of(dev))
@@ -271,7 +271,7 @@ class KVCache4:
         qt, qh = _heads("q", q, dev, T, H, self.head_dim, (torch.bfloat16,))
         if q.requires_grad:
             _refuse_grad()
-        tab, rows, stride = _table(table, dev)
+        tab, rows, stride = _table(table, dev, B)
         if rows < B:
             _bad("table", f"{rows} rows for {B} requests")
         given = out is not None

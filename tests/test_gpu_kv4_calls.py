@@ -147,3 +147,22 @@ def test_a_backward_pass_notices_that_a_saved_tensor_was_written_to():
         y = torch.empty_like(x)
         assert rope(x, pos, plan, out=y) is y
         cache.read(req, pos, table, k_out=y, v_out=torch.empty_like(y))
+
+
+@pytest.mark.parametrize("columns", [0, 3])
+def test_a_batch_of_no_requests_has_a_table_without_rows(columns):
+    cache = KVCache4(4, 32, 2, 64)
+    table = torch.zeros((0, columns), dtype=torch.int32, device="cuda")
+    none = i32([])
+    k = torch.zeros((0, 2, 64), device="cuda")
+    cache.append(k, k, none, none, table, rope=Rope(64))
+    assert all(t.shape == (0, 2, 64) for t in cache.read(none, none, table))
+    for T, max_q, max_kv in ((0, 0, 0), (5, 2, 70)):
+        q = torch.zeros((T, 4, 64), dtype=torch.bfloat16, device="cuda")
+        out, lse = cache.attend(q, i32([0]), none, table, max_q, max_kv, return_lse=True, out=torch.full_like(q, 3.0))
+        assert out.shape == q.shape and lse.shape == (T, 4) and (out == 3.0).all()
+    x = torch.zeros((1, 2, 64), device="cuda")                        # with a token or a request a row is needed
+    for bad in (lambda: cache.append(x, x, i32([0]), i32([0]), table), lambda: cache.read(i32([0]), i32([0]), table),
+                lambda: cache.attend(torch.zeros((1, 4, 64), dtype=torch.bfloat16, device="cuda"), i32([0, 1]), i32([1]), table, 1, 1)):
+        with pytest.raises(ValueError):
+            bad()
