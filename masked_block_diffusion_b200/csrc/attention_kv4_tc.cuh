@@ -766,7 +766,7 @@ attn_kv4_tc_kernel(const __grid_constant__ AttnKv4Params p) {
     uint32_t done = 0;
     while (walk.next(p, w)) {
       if (w.rq.bad) {
-        if (t == 0) kv4_poison(p, w.rq, w.h * p.group, p.group, HD, threadIdx.x - 64, 128);
+        if (t == 0) kv4_poison<HD>(p, w.rq, w.h * p.group, p.group, threadIdx.x - 64, 128);
       } else if (t == 0 || w.rq.n * p.group - 256 * w.tile > 128) {
         kv4_softmax_tile<HD>(p, w, tmem_slot, s_full, s_read, p_full, pv_done, q_full, smem + t * G::kQTile, flags, t, done);
         done += w.j1 - w.j0;

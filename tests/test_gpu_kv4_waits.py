@@ -87,3 +87,24 @@ def test_waits_of_the_few_row_kernel_that_run_out_lose_rows_and_nothing_else(han
     assert torch.equal(o, out) and torch.equal(z, lse)
     if most == 0:
         pytest.skip("no wait ran out in five calls: the path that loses rows was not taken")
+
+
+@pytest.mark.parametrize("d,h,hk,B", [(176, 4, 2, 150), (64, 16, 1, 37)])
+def test_answering_a_large_bad_request_does_not_keep_the_next_tile_waiting_for_long(handle, d, h, hk, B):
+    """60 000 rows of NaN for two KV heads with 2 heads of 176 each are 84 MB, for one with 16 heads of 64 123 MB. The limit
+    of 10 ms for them, 12 GB/s from one thread block, stands for the default of 2 s for 200 times as many."""
+    n, keys, many = 256, 500, 60000
+    cache, table, q, start = make(d, h, hk, 64, [many] + [n] * B, [1] + [keys] * B, seed=d)
+    lens = torch.full((B + 1,), keys, dtype=torch.int32, device="cuda")
+    lens[0] = -1
+    first = shares(d, h, hk, [1] + [n] * B, [0] + [keys] * B, False)[0]
+    assert [w.request for w in first[:hk]] == [0] * hk and first[hk].request == 1
+    torch.cuda.synchronize()
+    binding.dllm_set_wait_limit(handle, 10_000_000)
+    try:
+        out, lse = cache.attend(q, start, lens, table, n, keys, return_lse=True)
+        torch.cuda.synchronize()
+    finally:
+        binding.dllm_set_wait_limit(handle, 0)
+    assert torch.isnan(out[:many]).all() and torch.isnan(lse[:many]).all()
+    assert torch.isfinite(out[many:]).all() and torch.isfinite(lse[many:]).all()
