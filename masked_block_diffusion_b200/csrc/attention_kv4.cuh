@@ -63,6 +63,10 @@ struct AttnKv4Params {
   uint32_t mask_bf16;             // 0x00780078
 };
 
+// The largest score for which the reference m may stay: its weight is 2^14. Rounded down, since where numbers
+// are 16 apart m + 14 would become m + 16, and a weight of 2^16 is infinite in fp16.
+DLLM_DEV float kv4_above(float m) { return __fadd_rd(m, kKv4Low + 8.f); }
+
 // A request's queries and keys. bad: its row range holds, but not its lengths: every row becomes NaN.
 struct Kv4Req {
   int q0, n, kv;
@@ -411,7 +415,7 @@ attn_kv4_kernel(const __grid_constant__ AttnKv4Params p) {
           mx1 = fmaxf(mx1, fmaxf(s[u][nr][1], s[u][nr][3]));
         }
         // a new reference only when a score is more than 2^14 above it (the first visible key always is)
-        if (__any_sync(0xffffffffu, mx0 > m[nr][0] + (kKv4Low + 8.f) || mx1 > m[nr][1] + (kKv4Low + 8.f))) {
+        if (__any_sync(0xffffffffu, mx0 > kv4_above(m[nr][0]) || mx1 > kv4_above(m[nr][1]))) {
           float f[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {

@@ -314,50 +314,36 @@ struct Kv4Walk {
   }
 };
 
-// Tile t's softmax: thread (warp w, lane) owns row 32 (w % 4) + lane of the tile. `done` counts the blocks of
-// keys that went through the tile's barriers before.
-template <int HD>
-DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const uint32_t* tmem_slot, uint64_t* s_full,
-                               uint64_t* s_read, uint64_t* p_full, uint64_t* pv_done, uint64_t* q_full,
-                               uint8_t* q_smem, volatile int* flags, int t, uint32_t done) {
+// The blocks of keys of a tile from j on, one row per thread; m and l are the row's reference and sum so far. `lim` is
+// where the row's keys end, counted from the first block's first. False once a wait was given up.
+// A weight is 2^(s fac - m), with one fma. That takes the rounded reference off the exact product, which shifts all of
+// a row's weights alike and is nothing while the rounding is far below 1. With a reference of 2^25 it is not: the
+// largest weight would leave fp16's range, or vanish. So this loop leaves before the weights of a block whose
+// reference is above 2^22 in any row of the warp, and FAR's, which rounds the products first as the reference is
+// rounded, goes on from there. (Rounding them where needed in one loop: prompt pieces at head_dim 64 93.4 us
+// instead of 88.9.)
+template <int HD, bool FAR>
+DLLM_DEV bool kv4_softmax_blocks(float scale, int lim, int nblk, uint32_t lane_base, uint64_t* s_full, uint64_t* s_read,
+                                 uint64_t* p_full, uint64_t* pv_done, volatile int* flags, int t, uint32_t done, int& j,
+                                 float& m, float& l) {
   using G = AttnKv4TcCfg<HD>;
-  constexpr int BK = G::BK, CH = G::CH, NCH = BK / CH, CHUNKS = HD / 8;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row0 = 32 * (warp & 3), row = row0 + lane;
-  const int R = 256 * w.tile + 128 * t + row;
-  const Kv4Req& rq = w.rq;
-  const int g = w.h, nblk = w.j1 - w.j0, ks = w.j0 * BK, ke = w.j1 * BK;
-  const bool real = R < rq.n * p.group;
-  const int lim = real ? min(ke, kv4_row_limit(p, rq, R / p.group)) : ke;
-  // Q: the warp's 32 rows, copied along the rows; rows past the last are 0. A tile without keys needs none, and
-  // must not arrive: the issuer counts a phase of q_full for each work with keys and waits for every one.
-  if (nblk > 0) {
-    const long src = real ? (long)(rq.q0 + R / p.group) * p.q_tok + (g * p.group + R % p.group) * p.q_head : -1;
-#pragma unroll 2
-    for (int i = 0; i < CHUNKS; ++i) {
-      const int u = 32 * i + lane, r = u / CHUNKS, c = u - r * CHUNKS;
-      const long from = __shfl_sync(0xffffffffu, src, r);
-      copy16(kv4_chunk(q_smem, row0 + r, c), p.q + (from >= 0 ? from + 8 * c : 0), from >= 0 ? 16 : 0);
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&q_full[t]);
-  }
-  const float fac = p.scale_log2;
-  const uint32_t lane_base = *tmem_slot + ((uint32_t)row0 << 16);
+  constexpr int BK = G::BK, CH = G::CH, NCH = BK / CH;
+  const int lane = threadIdx.x & 31;
   const uint32_t o_col = lane_base + G::kOCol + t * HD;
-  float m = -INFINITY, l = 0.f;
-  bool ok = true;
+  const float fac = FAR ? 1.f : scale;
 #pragma unroll 1
-  for (int j = 0; j < nblk; ++j) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&s_full[G::bar(t, done + j)], G::par(done + j), flags))) { ok = false; break; }
+  for (; j < nblk; ++j) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&s_full[G::bar(t, done + j)], G::par(done + j), flags))) return false;
     tc_fence_after();
     const uint32_t s_col = lane_base + G::s_col(t, done + j);
     float s[CH];
-    const int seen = lim - (ks + j * BK);
+    const int seen = lim - j * BK;
     auto load = [&](int q) {
       kv4_load_scores(s_col + q * CH, s);
+      if (FAR) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) s[c] *= scale;
+      }
       if (seen < (q + 1) * CH) {
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -372,13 +358,15 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const u
       for (int c = 0; c < CH; ++c) top[c & 3] = fmaxf(top[c & 3], s[c]);
     }
     const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fac;
+    bool moved = j == 0;
     if (j == 0) {
       m = mx - kKv4Low;
     } else {
-      const bool need = mx > m + (kKv4Low + 8.f);
-      if (__any_sync(0xffffffffu, need)) {
+      const bool need = mx > kv4_above(m);
+      moved = __any_sync(0xffffffffu, need);
+      if (moved) {
         // O is stable once the product of the block before is done
-        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[G::bar(t, done + j - 1)], G::par(done + j - 1), flags))) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[G::bar(t, done + j - 1)], G::par(done + j - 1), flags))) return false;
         tc_fence_after();
         const float mn = need ? mx - kKv4Low : m;
         const float f = need ? exp2f(m - mn) : 1.0f;
@@ -394,6 +382,7 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const u
         m = mn;
       }
     }
+    if (!FAR && moved && __any_sync(0xffffffffu, fabsf(m) > 0x1p22f && m != -INFINITY)) return true;
     const float mb = m == -INFINITY ? 0.f : m;
     const uint64_t sc2 = pack_f32x2(fac, fac), mb2 = pack_f32x2(-mb, -mb);
     uint64_t sum[4] = {0, 0, 0, 0};   // pairs of fp32 sums
@@ -417,12 +406,11 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const u
         pk[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
       }
       if (q == NCH - 1 && j > 0 && !G::TWO) {   // P's columns are free once the product of the block before is done
-        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[G::bar(t, done + j - 1)], G::par(done + j - 1), flags))) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[G::bar(t, done + j - 1)], G::par(done + j - 1), flags))) return false;
         tc_fence_after();
       }
       kv4_store_weights(lane_base + G::p_col(t, done + j, q * CH), pk);
     }
-    if (!ok) break;
     float l0, l1;
     unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), l0, l1);
     l += l0 + l1;
@@ -431,6 +419,48 @@ DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const u
     __syncwarp();
     if (lane == 0) mbar_arrive(&p_full[G::bar(t, done + j)]);
   }
+  return true;
+}
+
+// Tile t's softmax: thread (warp w, lane) owns row 32 (w % 4) + lane of the tile. `done` counts the blocks of
+// keys that went through the tile's barriers before.
+template <int HD>
+DLLM_DEV void kv4_softmax_tile(const AttnKv4Params& p, const Kv4Work& w, const uint32_t* tmem_slot, uint64_t* s_full,
+                               uint64_t* s_read, uint64_t* p_full, uint64_t* pv_done, uint64_t* q_full,
+                               uint8_t* q_smem, volatile int* flags, int t, uint32_t done) {
+  using G = AttnKv4TcCfg<HD>;
+  constexpr int BK = G::BK, CHUNKS = HD / 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row0 = 32 * (warp & 3), row = row0 + lane;
+  const int R = 256 * w.tile + 128 * t + row;
+  const Kv4Req& rq = w.rq;
+  const int g = w.h, nblk = w.j1 - w.j0, ks = w.j0 * BK, ke = w.j1 * BK;
+  const bool real = R < rq.n * p.group;
+  const int lim = real ? min(ke, kv4_row_limit(p, rq, R / p.group)) : ke;
+  // Q: the warp's 32 rows, copied along the rows; rows past the last are 0. A tile without keys needs none, and
+  // must not arrive: the issuer counts a phase of q_full for each work with keys and waits for every one.
+  if (nblk > 0) {
+    const long src = real ? (long)(rq.q0 + R / p.group) * p.q_tok + (g * p.group + R % p.group) * p.q_head : -1;
+#pragma unroll 2
+    for (int i = 0; i < CHUNKS; ++i) {
+      const int u = 32 * i + lane, r = u / CHUNKS, c = u - r * CHUNKS;
+      const long from = __shfl_sync(0xffffffffu, src, r);
+      copy16(kv4_chunk(q_smem, row0 + r, c), p.q + (from >= 0 ? from + 8 * c : 0), from >= 0 ? 16 : 0);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_full[t]);
+  }
+  const uint32_t lane_base = *tmem_slot + ((uint32_t)row0 << 16);
+  const uint32_t o_col = lane_base + G::kOCol + t * HD;
+  float m = -INFINITY, l = 0.f;
+  int j = 0;
+  bool ok = kv4_softmax_blocks<HD, false>(p.scale_log2, lim - ks, nblk, lane_base, s_full, s_read, p_full, pv_done, flags, t,
+                                          done, j, m, l);
+  if (ok && j < nblk)
+    ok = kv4_softmax_blocks<HD, true>(p.scale_log2, lim - ks, nblk, lane_base, s_full, s_read, p_full, pv_done, flags, t, done,
+                                      j, m, l);
   if (ok && nblk > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[G::bar(t, done + nblk - 1)], G::par(done + nblk - 1), flags));
   if (!ok) flags[0] = 1;
   tc_fence_after();
