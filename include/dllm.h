@@ -333,7 +333,8 @@ typedef struct {
  *   NTK     theta * factor^(rotary_dim / (rotary_dim - 2)) in place of theta (rotary_dim >= 4);
  *   YARN    by parts: pairs that turn more than beta_fast times over original_ctx positions keep
  *           NONE's angle, pairs below beta_slow turns take LINEAR's, a linear ramp over the pair
- *           index lies between; magnitude = 0.1 ln(factor) + 1 (else 1).
+ *           index lies between, its ends rounded outwards to whole pairs and the lower one at least 0
+ *           (so pair 0 keeps NONE's angle); magnitude = 0.1 ln(factor) + 1 (else 1).
  * factor >= 1 (NONE ignores it); original_ctx, beta_fast and beta_slow are YARN's alone. */
 int dllm_rope_init(dllm_rope* out, int rotary_dim, int layout, double theta, int scaling, double factor,
                    double original_ctx, double beta_fast, double beta_slow);
@@ -352,13 +353,15 @@ int dllm_op_rope(const dllm_rope* rope, const void* x, int x_type, long long x_t
 /* A paged 4-bit cache of one layer (a host struct; the arrays are the caller's, 16-byte aligned):
  *   codes  uint8 [n_pages][2][n_kv_heads][page][head_dim / 2]    ([2]: K, V)
  *   scales uint8 [n_pages][2][n_kv_heads][page][head_dim / 16]
- * page: 16, 32, 64, 128 or 256 positions; head_dim: 64, 128 or 176; n_pages * page < 2^31.
+ * page: 16, 32, 64, 128 or 256 positions; head_dim: 64, 128 or 176; n_pages * page < 2^31;
+ * n_kv_heads <= 1024.
  * A scale byte b is shared by 16 consecutive dims and means the fp16 number with bits b << 7;
  * a dim's value is scale * (code - 8). The codes of dims 8 w .. 8 w + 7 are one little-endian
  * 32-bit word: dim 8 w + 2 j is nibble j, dim 8 w + 2 j + 1 nibble j + 4. Appending writes the
  * least scale with 7 * scale >= the group's largest magnitude and the nearest code in 1 .. 15
- * (ties to even); magnitudes beyond 17920 saturate, NaN is stored as 0. Every value is exact
- * in bf16.
+ * (ties to even); magnitudes beyond 17920 saturate, NaN is stored as 0, and a group whose largest
+ * magnitude is below 2^-147 may take scale 0 (its values are 0 under any scale). Every value is
+ * exact in bf16.
  * Page tables are device int32 [rows][table_stride]: position p of row r lies in page
  * table[r][p / page]. Rows may share pages (a common prefix), and layers may share a table. */
 typedef struct {
@@ -390,8 +393,8 @@ int dllm_op_read_kv4(const dllm_kv4* cache, const int32_t* req, const int32_t* p
  * q_start[b + 1] - 1 of q (bf16 [T][H][head_dim] with strides that are multiples of 8, 16-byte
  * aligned) and it sees positions 0 .. kv_len[b] - 1 of table row b: all of them, or with
  * causal = 1 query i of n those below kv_len[b] - n + i + 1 (its queries are the last n
- * positions). q_start [B + 1] and kv_len [B] are device int32. H is a multiple of n_kv_heads;
- * query head h reads KV head h / (H / n_kv_heads).
+ * positions). q_start [B + 1] and kv_len [B] are device int32. H is a multiple of n_kv_heads, at
+ * most 128 times it; query head h reads KV head h / (H / n_kv_heads). B <= 65535, T H < 2^31.
  *   out[t][h] (bf16, strides as q's) = softmax(scale * q k^T) v; a row that sees no key is 0.
  *   lse[t][h] (fp32 [T][H], or NULL) = the natural log of the sum of exp(scale * q k), -inf for a
  *   row that sees no key: it joins this result with attention over other keys.

@@ -134,6 +134,8 @@ DLLM_DEV uint32_t kv4_pack8(float (&v)[8], int& byte) {
 // cos and sin are there; a rotated chunk's partner comes later, out of the L1 cache, where
 // another thread's load has brought it. Bound by instruction issue (68% while SMs are busy): 10 600
 // tokens of 8 heads of 176 in bf16, three prompts, 38 us (26 without rotation), 77 MB; 64 tokens 3.3 us.
+// Part of the issue is work done twice: both lanes of a group find its scale, a rotated word is loaded by two threads, and at
+// the launch bounds' 40 registers the bf16 vector form spills (36 bytes a thread at 176 dims, 20 at 64 and 128).
 template <int HD, typename TI, bool VEC>
 __global__ void __launch_bounds__(512, sizeof(TI) == 2 ? 3 : 2)
 kv4_append_kernel(const __grid_constant__ RopeParams r, Kv4 c, Kv4Addr a, const TI* __restrict__ k, long k_tok,

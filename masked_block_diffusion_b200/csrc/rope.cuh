@@ -195,8 +195,10 @@ struct Raw8<float> {
 // Rotates tb tokens, all heads, in units of a head: VEC, 8 pairs (half layout), 8 elements
 // (interleaved) or 8 dims that are only copied; otherwise one pair or one dim. A thread's next load
 // is on its way while it works on the last one, the first while cos and sin are computed.
-// Bound by memory: 32768 tokens of 16 heads of 64 in bf16, half of each rotated, 31.5 us, 4.3 TB/s (a torch copy
-// of as many bytes 3.0); 64 tokens of 16 heads of 176 2.7 us, a launch's time.
+// 32768 tokens of 16 heads of 64 in bf16, half of each rotated: 31.3 us, 4.3 of 6.55 TB/s. Bound by issue (68% while
+// SMs are busy) and the L1 pipe (67%), not by memory: the launch bounds leave the bf16 vector form 40 registers, and it
+// spills 80 bytes a thread (fp32: 64 registers, 36 bytes); 2048 blocks are 2.3 waves. The bounds are for 512 threads,
+// which only tokens of more than 128 units need. 64 tokens of 16 heads of 176 2.6 us, a launch's time.
 // In place is fine: a unit reads everything it writes before writing it, and nothing else
 // reads it.
 template <typename TI, typename TO, bool VEC>
