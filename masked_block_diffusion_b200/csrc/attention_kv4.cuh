@@ -24,7 +24,7 @@
 // P is rounded to fp16 (11 bits) for O^T; the running maximum is kept 6 octaves low, so that
 // P up to 2^14 uses fp16's range and weights down to 2^-30 of the largest survive. Scores,
 // sums and accumulators are fp32.
-// Measured: one token of 64 requests over up to 4352 keys (16 heads, 8 KV heads of 176) 112 us, 3.0 TB/s of packed
+// Measured: one token of 64 requests over up to 4352 keys (16 heads, 8 KV heads of 176) 111 us, 3.0 TB/s of packed
 // cache; two tokens over 131072 keys (16 heads, 4 KV heads of 64) 37.1 us, 1.8 TB/s; one token over 4352
 // keys 12.4 us with the join. Issue (59% while SMs are busy) and the latency of dependent instructions with
 // 16 warps per SM bound the long calls.
